@@ -52,8 +52,9 @@
 extern "C" {
 #endif
 
-/* element types (MOE_Q8_0 and MOE_FP8_E4M3: expert weights of the decode path only) */
-enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_Q4_0 = 2, MOE_Q8_0 = 3, MOE_FP8_E4M3 = 4 };
+/* element types (MOE_Q8_0 and MOE_FP8_E4M3: expert weights of the decode path only; MOE_I8: signed
+ * 8-bit integer codes of moe_grouped_matmul_i8 only) */
+enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_Q4_0 = 2, MOE_Q8_0 = 3, MOE_FP8_E4M3 = 4, MOE_I8 = 5 };
 
 /* execution path (moe_shape_t.path) */
 enum {
@@ -398,6 +399,116 @@ int moe_cache_stats(moe_expert_cache_t* c, moe_cache_stats_t* out /* (host) */, 
 /* Forgets every resident expert: the next call's launches find none (the map
  * is cleared on its stream first); copies in flight still complete. */
 int moe_cache_flush(moe_expert_cache_t* c);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The layer's parts as operators of their own: for experts whose form is not
+ * the SwiGLU of moe_forward, for training (both directions of the products
+ * and of the combine), and for experts held in 8-bit integers at any batch
+ * size.  moe_route makes the tables they read.
+ *
+ * Segments.  An expert-sorted order of `rows` rows gives expert e the rows
+ * offsets[e] .. offsets[e] + counts[e] - 1 (moe_route's padded order: its
+ * offsets and counts).  With counts NULL a segment ends where the next one
+ * starts (offsets[e + 1]); then the order must hold no padding.  offsets has
+ * E + 1 entries with counts NULL and at least E otherwise.  The tables are
+ * device data, so their contents are not checked by an error code: a segment
+ * is cut to [0, rows), a negative count is an empty segment, and segments
+ * that overlap leave the shared rows of y and dx to either of their experts.
+ * Rows in no segment are neither read nor written.
+ *
+ * Row lookup.  With row_ids (int32 [rows], moe_route's sorted_ids with
+ * row_div = top_k), sorted row r reads row row_ids[r] / row_div of x, which
+ * has x_rows rows; a row_ids[r] that is negative or at least
+ * x_rows * row_div stands for a row of zeros.  The same row may be looked up
+ * any number of times.  With row_ids NULL sorted row r is row r of x:
+ * x_rows must be `rows` and row_div 1.
+ *
+ * All matrices are dense and row-major.  An output may not overlap an input,
+ * the workspace or another output.  Every sum is formed in one fixed order
+ * (no atomics), so repeated calls give the same bits.  `rows` may be 0.
+ */
+typedef struct {
+  int32_t rows;      /* rows of the sorted order, 0 <= rows <= 33554432 */
+  int32_t N, K;      /* w[e] is [N, K]: K values in, N values out; 1 .. 1048576 each
+                        (MOE_I8: K <= 131071, so that no sum of products of codes leaves 32 bits) */
+  int32_t E;         /* experts, 1 .. 256 (1: one dense product over the segment) */
+  int32_t x_rows;    /* rows of x, 0 .. 33554432 */
+  int32_t row_div;   /* 1 .. 256 */
+  int32_t x_dtype;   /* MOE_F32 | MOE_BF16 | MOE_I8: x and w (dy and dx likewise) */
+  int32_t out_dtype; /* y, and dw of the backward call: MOE_F32, or MOE_BF16 unless x_dtype is MOE_F32 */
+} moe_grouped_shape_t;
+
+/* Bytes of workspace that the calls with shape *s need (the most any of them
+ * does; host call, no GPU access). */
+int moe_grouped_workspace_size(const moe_grouped_shape_t* s, size_t* bytes /* host */);
+
+/* y[r, n] = sum_k x[row(r), k] * w[e, n, k] for the rows r of each expert e.
+ *   x [x_rows, K], w [E, N, K] (x_dtype: MOE_F32 or MOE_BF16), y [rows, N]
+ * Products are summed in fp32 and rounded once. */
+int moe_grouped_matmul(const moe_grouped_shape_t* s, const void* x, const int32_t* row_ids,
+                       const int32_t* offsets, const int32_t* counts, const void* w, void* y,
+                       void* workspace, size_t ws_bytes, void* stream);
+
+/* The gradients of moe_grouped_matmul for dy [rows, N]:
+ *   dx[r, k]    = sum_n dy[r, n] * w[e, n, k]           dx [rows, K], x_dtype, in sorted order
+ *   dw[e, n, k] = sum over e's rows r of dy[r, n] * x[row(r), k]     dw [E, N, K], out_dtype
+ * dx or dw may be NULL (not both, while there are rows): that gradient is not formed, and w (needed
+ * for dx only) or x and row_ids (needed for dw only) may be NULL with it.
+ * dw is written whole; experts without rows get zeros.  The gradient of a
+ * gathered x is moe_combine of dx with weights NULL. */
+int moe_grouped_matmul_backward(const moe_grouped_shape_t* s, const void* dy, const void* x,
+                                const int32_t* row_ids, const int32_t* offsets, const int32_t* counts,
+                                const void* w, void* dx, void* dw, void* workspace, size_t ws_bytes,
+                                void* stream);
+
+/* 8-bit codes of each row of x [rows, cols] (MOE_F32 or MOE_BF16):
+ *   scale[r] = max |x[r, :]| / 127, rounded to fp32;
+ *   q[r, c]  = the integer nearest x[r, c] / scale[r] (ties to the even one), within +-127.
+ * A row of zeros (or one whose scale rounds to zero) has scale 0 and codes
+ * 0; a row that holds a NaN or an infinity has scale NaN and codes 0, so that
+ * its products are NaN.  0 <= rows <= 33554432, 1 <= cols <= 1048576. */
+int moe_quantize_rows(int32_t rows, int32_t cols, int32_t x_dtype, const void* x, int8_t* q, float* scale,
+                      void* stream);
+
+/* The forward product on 8-bit codes (shape x_dtype MOE_I8):
+ *   y[r, n] = x_scale[row(r)] * w_scale[e, n] * sum_k xq[row(r), k] * wq[e, n, k]
+ *   xq int8 [x_rows, K], x_scale f32 [x_rows] (moe_quantize_rows);
+ *   wq int8 [E, N, K], w_scale f32 [E, N]; y [rows, N]
+ * The sum is exact; the scales are applied in fp32, x_scale first.  A row
+ * that row_ids stands for zeros has the product 0. */
+int moe_grouped_matmul_i8(const moe_grouped_shape_t* s, const int8_t* xq, const float* x_scale,
+                          const int32_t* row_ids, const int32_t* offsets, const int32_t* counts,
+                          const int8_t* wq, const float* w_scale, void* y, void* workspace, size_t ws_bytes,
+                          void* stream);
+
+/* The way back from the sorted order to the tokens. */
+typedef struct {
+  int32_t T;         /* tokens, 0 <= T <= 1048576 */
+  int32_t top_k;     /* rows per token, 1 .. 256, T * top_k <= 16777216 */
+  int32_t H;         /* values per row, 1 .. 1048576 */
+  int32_t rows;      /* rows of y, 0 <= rows <= 33554432 */
+  int32_t y_dtype;   /* MOE_F32 | MOE_BF16: y (and dy) */
+  int32_t out_dtype; /* MOE_F32 | MOE_BF16: out (and dout) */
+} moe_combine_shape_t;
+
+/* out[t, :] = sum_j weights[t, j] * y[inv[t, j], :], in the order of j, in fp32.
+ *   y [rows, H]; inv int32 [T, top_k] (moe_route's inv); weights f32 [T, top_k]
+ *   (moe_route's topk_w), or NULL for weights of 1; out [T, H]
+ * An inv outside [0, rows) is a dropped assignment: it adds nothing (a token
+ * whose assignments are all dropped gets zeros). */
+int moe_combine(const moe_combine_shape_t* s, const void* y, const int32_t* inv, const float* weights,
+                void* out, void* stream);
+
+/* The gradients of moe_combine for dout [T, H] (out_dtype):
+ *   dy[inv[t, j], :] = weights[t, j] * dout[t, :]       dy [rows, H], y_dtype
+ *   dweights[t, j]   = sum_h dout[t, h] * y[inv[t, j], h]    f32 [T, top_k]; 0 when dropped
+ * dy or dweights may be NULL (not both, while there are rows); y is needed for dweights only.  Rows
+ * of dy that no assignment names are left as they were, and the entries of
+ * inv within [0, rows) must differ from each other (a row named twice would
+ * get either one's gradient). */
+int moe_combine_backward(const moe_combine_shape_t* s, const void* dout, const void* y, const int32_t* inv,
+                         const float* weights, void* dy, float* dweights, void* stream);
 
 /* The hipError_t value behind the most recent MOE_ERR_HIP returned to the
  * calling thread (0 if there was none).  Host call. */

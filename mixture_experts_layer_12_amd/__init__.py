@@ -18,7 +18,7 @@ LIB_DIR = os.path.join(os.path.dirname(os.path.abspath(__file__)), "lib")
 LIB_PATH = os.path.join(LIB_DIR, "libmoe.so")
 
 # enums of moe.h
-MOE_F32, MOE_BF16, MOE_Q4_0, MOE_Q8_0, MOE_FP8_E4M3 = 0, 1, 2, 3, 4
+MOE_F32, MOE_BF16, MOE_Q4_0, MOE_Q8_0, MOE_FP8_E4M3, MOE_I8 = 0, 1, 2, 3, 4, 5
 MOE_PATH_AUTO, MOE_PATH_DECODE, MOE_PATH_PREFILL, MOE_PATH_DECODE_FUSED = 0, 1, 2, 3
 MOE_OK, MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_DTYPE, MOE_ERR_ALIGN, MOE_ERR_WORKSPACE, MOE_ERR_HIP = (
     0, -1, -2, -3, -4, -5, -6)
@@ -27,12 +27,15 @@ MOE_ERR_NOT_PINNED = -8
 MOE_ERR_HOST_ALLOC = -9
 MOE_NOALLOC_SCRATCH_BYTES = 64 << 20
 
-DTYPES = {"f32": MOE_F32, "bf16": MOE_BF16, "q4_0": MOE_Q4_0, "q8_0": MOE_Q8_0, "fp8_e4m3": MOE_FP8_E4M3}
+DTYPES = {"f32": MOE_F32, "bf16": MOE_BF16, "q4_0": MOE_Q4_0, "q8_0": MOE_Q8_0, "fp8_e4m3": MOE_FP8_E4M3,
+          "i8": MOE_I8}
 EXPORTED = ("moe_workspace_size", "moe_dispatch_dims", "moe_route", "moe_forward", "moe_forward_profiled",
             "moe_last_hip_error", "moe_strerror", "moe_resolve_path", "moe_sparse_workspace_size",
             "moe_forward_channel_sparse", "moe_forward_tables", "moe_route_workspace_size",
             "moe_probe_read", "moe_probe_mfma_bf16", "moe_forward_noalloc", "moe_cache_region_bytes",
-            "moe_cache_create", "moe_cache_destroy", "moe_forward_cached", "moe_cache_stats", "moe_cache_flush")
+            "moe_cache_create", "moe_cache_destroy", "moe_forward_cached", "moe_cache_stats", "moe_cache_flush",
+            "moe_grouped_workspace_size", "moe_grouped_matmul", "moe_grouped_matmul_backward", "moe_quantize_rows",
+            "moe_grouped_matmul_i8", "moe_combine", "moe_combine_backward")
 
 
 class moe_shape_t(ctypes.Structure):
@@ -59,6 +62,14 @@ class moe_host_experts_t(ctypes.Structure):
 class moe_cache_stats_t(ctypes.Structure):
     _fields_ = [(n, ctypes.c_uint64) for n in (
         "lookups", "hits", "misses", "prefetches", "prefetch_hits", "bytes_copied")]
+
+
+class moe_grouped_shape_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("rows", "N", "K", "E", "x_rows", "row_div", "x_dtype", "out_dtype")]
+
+
+class moe_combine_shape_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "top_k", "H", "rows", "y_dtype", "out_dtype")]
 
 
 class MoeError(RuntimeError):
@@ -125,6 +136,20 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moe_cache_flush.restype = ctypes.c_int
     lib.moe_resolve_path.argtypes = [P(moe_shape_t)]
     lib.moe_resolve_path.restype = ctypes.c_int
+    lib.moe_grouped_workspace_size.argtypes = [P(moe_grouped_shape_t), P(sz)]
+    lib.moe_grouped_workspace_size.restype = ctypes.c_int
+    lib.moe_grouped_matmul.argtypes = [P(moe_grouped_shape_t)] + [vp] * 7 + [sz, vp]
+    lib.moe_grouped_matmul.restype = ctypes.c_int
+    lib.moe_grouped_matmul_backward.argtypes = [P(moe_grouped_shape_t)] + [vp] * 9 + [sz, vp]
+    lib.moe_grouped_matmul_backward.restype = ctypes.c_int
+    lib.moe_quantize_rows.argtypes = [i32, i32, i32, vp, vp, vp, vp]
+    lib.moe_quantize_rows.restype = ctypes.c_int
+    lib.moe_grouped_matmul_i8.argtypes = [P(moe_grouped_shape_t)] + [vp] * 9 + [sz, vp]
+    lib.moe_grouped_matmul_i8.restype = ctypes.c_int
+    lib.moe_combine.argtypes = [P(moe_combine_shape_t)] + [vp] * 5
+    lib.moe_combine.restype = ctypes.c_int
+    lib.moe_combine_backward.argtypes = [P(moe_combine_shape_t)] + [vp] * 7
+    lib.moe_combine_backward.restype = ctypes.c_int
     lib.moe_strerror.argtypes = [ctypes.c_int]
     lib.moe_strerror.restype = ctypes.c_char_p
     _lib = lib
@@ -385,3 +410,158 @@ def alloc_workspace(shape: moe_shape_t, device="cuda"):
     """A workspace of moe_workspace_size(shape) bytes (torch uint8 tensor; contents irrelevant)."""
     import torch
     return torch.empty(max(moe_workspace_size(shape), 256), dtype=torch.uint8, device=device)
+
+
+# ------------------------------------------------- the layer's parts as operators --
+
+def make_grouped_shape(rows, N, K, E, x_rows=None, row_div=1, x_dtype="bf16", out_dtype="bf16") -> moe_grouped_shape_t:
+    """Shape of the grouped expert products; ``x_rows`` defaults to ``rows`` (no row lookup)."""
+    conv = lambda d: DTYPES[d] if isinstance(d, str) else int(d)
+    return moe_grouped_shape_t(int(rows), int(N), int(K), int(E), int(rows if x_rows is None else x_rows),
+                               int(row_div), conv(x_dtype), conv(out_dtype))
+
+
+def make_combine_shape(T, top_k, H, rows, y_dtype="bf16", out_dtype="bf16") -> moe_combine_shape_t:
+    conv = lambda d: DTYPES[d] if isinstance(d, str) else int(d)
+    return moe_combine_shape_t(int(T), int(top_k), int(H), int(rows), conv(y_dtype), conv(out_dtype))
+
+
+def moe_grouped_workspace_size(shape: moe_grouped_shape_t) -> int:
+    n = ctypes.c_size_t(0)
+    rc = load_library().moe_grouped_workspace_size(ctypes.byref(shape), ctypes.byref(n))
+    if rc:
+        raise MoeError(rc, "moe_grouped_workspace_size")
+    return n.value
+
+
+def alloc_grouped_workspace(shape: moe_grouped_shape_t, device="cuda"):
+    """A workspace of moe_grouped_workspace_size(shape) bytes (contents irrelevant)."""
+    import torch
+    return torch.empty(max(moe_grouped_workspace_size(shape), 256), dtype=torch.uint8, device=device)
+
+
+_TORCH_NAMES = {MOE_F32: "torch.float32", MOE_BF16: "torch.bfloat16", MOE_I8: "torch.int8", "i32": "torch.int32"}
+
+
+def _operands(where: str, *specs):
+    """Checks the tensors among ``specs`` ((name, value, dtype code, elements) each): dense, on one GPU, of the
+    type and size that the shape says.  Raw addresses and None pass.  Returns that GPU's index, or None."""
+    device = None
+    for name, t, dtype, n in specs:
+        if t is None or isinstance(t, int):
+            continue
+        if not t.is_contiguous():
+            raise ValueError(f"{where}: {name} is not contiguous")
+        if str(t.dtype) != _TORCH_NAMES[dtype]:
+            raise ValueError(f"{where}: {name} has type {t.dtype}, the shape says {_TORCH_NAMES[dtype]}")
+        if t.numel() < n:
+            raise ValueError(f"{where}: {name} has {t.numel()} elements, the shape needs {n}")
+        index = t.get_device()
+        if index < 0:
+            raise ValueError(f"{where}: {name} is not on a GPU")
+        if device is None:
+            device = index
+        elif index != device:
+            raise ValueError(f"{where}: {name} is on another GPU than the operands before it")
+    return device
+
+
+def _on_device(device, stream, call):
+    """call(stream handle) with ``device`` (an index, or None) current; stream None is that device's current one."""
+    import torch
+    if device is None or device == torch.cuda.current_device():
+        return call(_stream(stream))
+    with torch.cuda.device(device):
+        return call(_stream(stream))
+
+
+def _grouped_specs(shape, x_name, x, row_ids, offsets, counts):
+    return ((x_name, x, shape.x_dtype, shape.x_rows * shape.K), ("row_ids", row_ids, "i32", shape.rows),
+            ("offsets", offsets, "i32", shape.E + (counts is None)), ("counts", counts, "i32", shape.E))
+
+
+def moe_grouped_matmul(shape: moe_grouped_shape_t, x, row_ids, offsets, counts, w, y, workspace, ws_bytes=None,
+                       stream=None, check=True) -> int:
+    """y[r] = x[row(r)] . w[e]^T over the segments; ``row_ids`` and ``counts`` may be None."""
+    dev = _operands("moe_grouped_matmul", *_grouped_specs(shape, "x", x, row_ids, offsets, counts),
+                    ("w", w, shape.x_dtype, shape.E * shape.N * shape.K), ("y", y, shape.out_dtype, shape.rows * shape.N))
+    nb = _nbytes(workspace) if ws_bytes is None else ws_bytes
+    rc = _on_device(dev, stream, lambda st: load_library().moe_grouped_matmul(
+        ctypes.byref(shape), _ptr(x), _ptr(row_ids), _ptr(offsets), _ptr(counts), _ptr(w), _ptr(y), _ptr(workspace),
+        nb, st))
+    if check and rc:
+        raise MoeError(rc, "moe_grouped_matmul")
+    return rc
+
+
+def moe_grouped_matmul_backward(shape: moe_grouped_shape_t, dy, x, row_ids, offsets, counts, w, dx, dw, workspace,
+                                ws_bytes=None, stream=None, check=True) -> int:
+    """The gradients dx (sorted order) and dw of moe_grouped_matmul; either may be None."""
+    size = shape.E * shape.N * shape.K
+    dev = _operands("moe_grouped_matmul_backward", *_grouped_specs(shape, "x", x, row_ids, offsets, counts),
+                    ("dy", dy, shape.x_dtype, shape.rows * shape.N), ("w", w, shape.x_dtype, size),
+                    ("dx", dx, shape.x_dtype, shape.rows * shape.K), ("dw", dw, shape.out_dtype, size))
+    nb = _nbytes(workspace) if ws_bytes is None else ws_bytes
+    rc = _on_device(dev, stream, lambda st: load_library().moe_grouped_matmul_backward(
+        ctypes.byref(shape), _ptr(dy), _ptr(x), _ptr(row_ids), _ptr(offsets), _ptr(counts), _ptr(w), _ptr(dx),
+        _ptr(dw), _ptr(workspace), nb, st))
+    if check and rc:
+        raise MoeError(rc, "moe_grouped_matmul_backward")
+    return rc
+
+
+def moe_quantize_rows(x, q, scale, stream=None, check=True) -> int:
+    """8-bit codes ``q`` and fp32 ``scale`` of each row of the matrix ``x`` (float32 or bfloat16, two dimensions)."""
+    if x.dim() != 2 or str(x.dtype) not in ("torch.float32", "torch.bfloat16"):
+        raise ValueError("moe_quantize_rows: x is not a float32 or bfloat16 matrix")
+    dt = MOE_F32 if str(x.dtype) == "torch.float32" else MOE_BF16
+    rows, cols = x.shape
+    dev = _operands("moe_quantize_rows", ("x", x, dt, rows * cols), ("q", q, MOE_I8, rows * cols),
+                    ("scale", scale, MOE_F32, rows))
+    rc = _on_device(dev, stream, lambda st: load_library().moe_quantize_rows(rows, cols, dt, _ptr(x), _ptr(q),
+                                                                             _ptr(scale), st))
+    if check and rc:
+        raise MoeError(rc, "moe_quantize_rows")
+    return rc
+
+
+def moe_grouped_matmul_i8(shape: moe_grouped_shape_t, xq, x_scale, row_ids, offsets, counts, wq, w_scale, y, workspace,
+                          ws_bytes=None, stream=None, check=True) -> int:
+    """The forward product on 8-bit codes with scales for each row of ``xq`` and each output channel of ``wq``."""
+    dev = _operands("moe_grouped_matmul_i8", *_grouped_specs(shape, "xq", xq, row_ids, offsets, counts),
+                    ("x_scale", x_scale, MOE_F32, shape.x_rows), ("wq", wq, MOE_I8, shape.E * shape.N * shape.K),
+                    ("w_scale", w_scale, MOE_F32, shape.E * shape.N), ("y", y, shape.out_dtype, shape.rows * shape.N))
+    nb = _nbytes(workspace) if ws_bytes is None else ws_bytes
+    rc = _on_device(dev, stream, lambda st: load_library().moe_grouped_matmul_i8(
+        ctypes.byref(shape), _ptr(xq), _ptr(x_scale), _ptr(row_ids), _ptr(offsets), _ptr(counts), _ptr(wq),
+        _ptr(w_scale), _ptr(y), _ptr(workspace), nb, st))
+    if check and rc:
+        raise MoeError(rc, "moe_grouped_matmul_i8")
+    return rc
+
+
+def moe_combine(shape: moe_combine_shape_t, y, inv, weights, out, stream=None, check=True) -> int:
+    """out[t] = sum_j weights[t, j] * y[inv[t, j]]; ``weights`` None means 1."""
+    n = shape.T * shape.top_k
+    dev = _operands("moe_combine", ("y", y, shape.y_dtype, shape.rows * shape.H), ("inv", inv, "i32", n),
+                    ("weights", weights, MOE_F32, n), ("out", out, shape.out_dtype, shape.T * shape.H))
+    rc = _on_device(dev, stream, lambda st: load_library().moe_combine(
+        ctypes.byref(shape), _ptr(y), _ptr(inv), _ptr(weights), _ptr(out), st))
+    if check and rc:
+        raise MoeError(rc, "moe_combine")
+    return rc
+
+
+def moe_combine_backward(shape: moe_combine_shape_t, dout, y, inv, weights, dy, dweights, stream=None,
+                         check=True) -> int:
+    """The gradients dy and dweights of moe_combine; either may be None (``y`` is read for dweights only)."""
+    n = shape.T * shape.top_k
+    dev = _operands("moe_combine_backward", ("dout", dout, shape.out_dtype, shape.T * shape.H),
+                    ("y", y, shape.y_dtype, shape.rows * shape.H), ("inv", inv, "i32", n),
+                    ("weights", weights, MOE_F32, n), ("dy", dy, shape.y_dtype, shape.rows * shape.H),
+                    ("dweights", dweights, MOE_F32, n))
+    rc = _on_device(dev, stream, lambda st: load_library().moe_combine_backward(
+        ctypes.byref(shape), _ptr(dout), _ptr(y), _ptr(inv), _ptr(weights), _ptr(dy), _ptr(dweights), st))
+    if check and rc:
+        raise MoeError(rc, "moe_combine_backward")
+    return rc

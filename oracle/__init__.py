@@ -30,8 +30,9 @@ Modules:
   moe     -- vectorised fp64 reference (numpy), including the budgeted
              channel-sparse experts
   loops   -- pure-Python brute force for tiny shapes
+  grouped -- the separate operators: grouped products and their gradients, 8-bit codes, combine
 """
-from . import formats, moe, loops  # noqa: F401
+from . import formats, grouped, moe, loops  # noqa: F401
 from .moe import (  # noqa: F401
     router_logits, softmax, select_topk, renormalize, route, near_ties,
     silu, swiglu_ffn, moe_forward, moe_forward_tokens, dispatch, dense_gate_matrix,
