@@ -15,40 +15,6 @@ namespace moe {
 
 namespace {
 
-typedef int i32x4_t __attribute__((ext_vector_type(4)));
-typedef int i32x16_t __attribute__((ext_vector_type(16)));
-typedef short s16x4_t __attribute__((ext_vector_type(4)));
-
-template <int DT> struct Elem;
-template <> struct Elem<DT_F32> { typedef float type; typedef f32x16_t acc; };
-template <> struct Elem<DT_BF16> { typedef uint16_t type; typedef f32x16_t acc; };
-template <> struct Elem<DT_I8> { typedef int8_t type; typedef i32x16_t acc; };
-
-__device__ __forceinline__ i32x16_t mfma32_i8(u32x4_t a, u32x4_t b, i32x16_t c) {
-  return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4_t, a), __builtin_bit_cast(i32x4_t, b), c, 0,
-                                               0, 0);
-}
-
-// acc += A x B over the values of q that 16 bytes a lane hold: lanes 0-31 the
-// first 16 bytes of each row, lanes 32-63 the next.  fp32 takes four MFMAs of
-// two values of q each.
-template <int DT, class Acc>
-__device__ __forceinline__ void mma16(u32x4_t a, u32x4_t b, Acc& c) {
-  if constexpr (DT == DT_BF16) c = mfma32_bf16(a, b, c);
-  else if constexpr (DT == DT_I8) c = mfma32_i8(a, b, c);
-  else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a[j]), __uint_as_float(b[j]), c, 0, 0, 0);
-  }
-}
-
-template <int OUT>
-__device__ __forceinline__ void store_out(void* out, size_t i, float v) {
-  if constexpr (OUT == DT_F32) reinterpret_cast<float*>(out)[i] = v;
-  else reinterpret_cast<uint16_t*>(out)[i] = uint16_t(f32_to_bf16(v));
-}
-
 // Up to 16 bytes from p, which need not be aligned: the first n elements (all
 // of a chunk's, or fewer at the end of a row), the others zero.
 template <class T>
@@ -134,6 +100,8 @@ __global__ void __launch_bounds__(ATHREADS) grouped_any_kernel(GroupedArgs a, lo
   const int n_ct = (n_cols + AT - 1) / AT;
   const int n_mt = (a.N + AT - 1) / AT;                          // dw: tiles along m
 
+  RowTiles tiles(a, AT);
+  if constexpr (WHICH != GM_GRAD_W) n_items = long(tiles.total) * n_ct;
   for (long item = blockIdx.x; item < n_items; item += gridDim.x) {
     int e, m0 = 0, m_end, row0 = 0, n_q;          // tile rows m0 .. m_end - 1; dw: first sorted row; extent of q
     const int n0 = int(item % n_ct) * AT;
@@ -146,8 +114,7 @@ __global__ void __launch_bounds__(ATHREADS) grouped_any_kernel(GroupedArgs a, lo
       row0 = s.begin;
       n_q = s.n;
     } else {
-      RowTile rt;
-      if (!find_row_tile(a, item / n_ct, AT, rt)) return;       // the later items lie past the end as well
+      const RowTile rt = tiles.at(int(item / n_ct), AT);
       e = rt.e;
       m0 = rt.begin;
       m_end = m0 + min(rt.n, AT);
@@ -166,7 +133,7 @@ __global__ void __launch_bounds__(ATHREADS) grouped_any_kernel(GroupedArgs a, lo
         const int m = m0 + r;
         const int src = m >= m_end ? -1 : (WHICH == GM_FORWARD ? source_row(a, m) : m);
         pa[i] = src < 0 ? nullptr : (WHICH == GM_FORWARD ? x + size_t(src) * a.K : dy + size_t(src) * a.N);
-        if (DT == DT_I8 && (tid & 7) == 0) row_scale[r] = src < 0 ? 0.f : a.x_scale[src];
+        if (WHICH == GM_FORWARD && (tid & 7) == 0) row_scale[r] = src < 0 ? 0.f : (DT == DT_I8 ? a.x_scale[src] : 1.f);
       }
       if constexpr (BQ) pb[i] = n0 + r < n_cols ? w + size_t(n0 + r) * a.K : nullptr;
     }
@@ -251,7 +218,7 @@ __global__ void __launch_bounds__(ATHREADS) grouped_any_kernel(GroupedArgs a, lo
           if (m0 + r >= m_end) continue;
           float v;
           if constexpr (DT == DT_I8) v = float(acc[i][j][q]) * row_scale[r] * ws;
-          else v = acc[i][j][q];
+          else v = WHICH == GM_FORWARD && row_scale[r] == 0.f ? 0.f : acc[i][j][q];   // rows that stand for zeros
           store_out<OUT>(a.out, out0 + size_t(m0 + r) * n_cols + n, v);
         }
     }
@@ -277,6 +244,7 @@ size_t grouped_workspace(const GroupedArgs&, int, int, int) { return 0; }
 
 hipError_t launch_grouped(const GroupedArgs& a, int which, int in_dt, int out_dt, void*, hipStream_t st) {
   if (which != GM_GRAD_W && a.rows == 0) return hipSuccess;
+  if (grouped_tile_fits(a, which, in_dt)) return launch_grouped_tile(a, which, in_dt, out_dt, st);
   if (in_dt == DT_I8)
     return out_dt == DT_F32 ? launch_any<DT_I8, DT_F32, GM_FORWARD>(a, st) : launch_any<DT_I8, DT_BF16, GM_FORWARD>(a, st);
   if (which == GM_FORWARD) {

@@ -9,6 +9,41 @@ namespace moe {
 enum : int { DT_I8 = 5 };                       // MOE_I8
 enum : int { GM_FORWARD = 0, GM_GRAD_X = 1, GM_GRAD_W = 2 };   // which product
 
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+typedef int i32x16_t __attribute__((ext_vector_type(16)));
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+
+// Element types: how they lie in memory and what their products are summed in.
+template <int DT> struct Elem;
+template <> struct Elem<DT_F32> { typedef float type; typedef f32x16_t acc; };
+template <> struct Elem<DT_BF16> { typedef uint16_t type; typedef f32x16_t acc; };
+template <> struct Elem<DT_I8> { typedef int8_t type; typedef i32x16_t acc; };
+
+__device__ __forceinline__ i32x16_t mfma32_i8(u32x4_t a, u32x4_t b, i32x16_t c) {
+  return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4_t, a), __builtin_bit_cast(i32x4_t, b), c, 0,
+                                               0, 0);
+}
+
+// acc += A x B over the values of q that 16 bytes a lane hold: lanes 0-31 the
+// first 16 bytes of each row, lanes 32-63 the next.  fp32 takes four MFMAs of
+// two values of q each.
+template <int DT, class Acc>
+__device__ __forceinline__ void mma16(u32x4_t a, u32x4_t b, Acc& c) {
+  if constexpr (DT == DT_BF16) c = mfma32_bf16(a, b, c);
+  else if constexpr (DT == DT_I8) c = mfma32_i8(a, b, c);
+  else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a[j]), __uint_as_float(b[j]), c, 0, 0, 0);
+  }
+}
+
+template <int OUT>
+__device__ __forceinline__ void store_out(void* out, size_t i, float v) {
+  if constexpr (OUT == DT_F32) reinterpret_cast<float*>(out)[i] = v;
+  else reinterpret_cast<uint16_t*>(out)[i] = uint16_t(f32_to_bf16(v));
+}
+
 struct GroupedArgs {
   const void* x;            // [x_rows, K] (forward, dw)
   const void* dy;           // [rows, N] (dx, dw)
@@ -20,6 +55,8 @@ struct GroupedArgs {
   const float* x_scale;     // 8-bit: [x_rows]
   const float* w_scale;     // 8-bit: [E, N]
   int rows, N, K, E, x_rows, row_div;
+  unsigned div_mul;         // n / row_div = mulhi(2 n, div_mul) >> div_shift for 0 <= n < 2^31
+  int div_shift;
 };
 
 // Expert e's segment [begin, begin + n) cut to [0, rows): whatever the tables
@@ -34,66 +71,75 @@ __device__ __forceinline__ Segment segment_of(const GroupedArgs& a, int e) {
   return Segment{int(lo), int(hi - lo)};
 }
 
-// Row of x that sorted row r reads, or -1 for a row of zeros.
-__device__ __forceinline__ int source_row(const GroupedArgs& a, int r) {
-  if (!a.row_ids) return r;
-  const int id = a.row_ids[r];
-  const int s = id / a.row_div;
-  return id >= 0 && s < a.x_rows ? s : -1;
+// Row of x that an entry of row_ids stands for, or -1 for a row of zeros.
+__device__ __forceinline__ int source_of(const GroupedArgs& a, int id) {
+  const int s = int(__umulhi(unsigned(id) << 1, a.div_mul) >> a.div_shift);
+  return ((id >= 0) & (s < a.x_rows)) ? s : -1;
 }
 
-// Row tile `idx` of the list that holds ceil(n / tile) tiles for each
-// expert's segment, in order: found by every wave for itself, four experts a
-// lane, with a prefix sum over the lanes.  False past the end of the list.
+// Row of x that sorted row r reads, or -1.
+__device__ __forceinline__ int source_row(const GroupedArgs& a, int r) {
+  if (!a.row_ids) return r;
+  return source_of(a, a.row_ids[r]);
+}
+
+// The list that holds ceil(n / tile) row tiles for each expert's segment, in
+// order.  Every wave looks it up for itself: four experts a lane, with a
+// prefix sum over the lanes.
 struct RowTile {
   int e;         // expert
   int begin;     // first sorted row of the tile
   int n;         // rows from there to the end of the segment
-  int in_seg;    // tile number within the segment
-  int seg_n;     // rows of the whole segment
 };
-__device__ __forceinline__ bool find_row_tile(const GroupedArgs& a, long idx, int tile, RowTile& out) {
-  const int lane = threadIdx.x & 63;
-  Segment s[4];
-  int t[4], sum = 0;
+struct RowTiles {
+  Segment s[4];  // segments of experts 4 lane .. 4 lane + 3
+  int t[4];      // their tiles
+  int first;     // tiles before them
+  int sum;       // their sum
+  int total;     // tiles of all experts
+
+  __device__ __forceinline__ RowTiles(const GroupedArgs& a, int tile) {
+    const int lane = threadIdx.x & 63;
+    sum = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int e = 4 * lane + i;
-    s[i] = e < a.E ? segment_of(a, e) : Segment{0, 0};
-    t[i] = (s[i].n + tile - 1) / tile;
-    sum += t[i];
-  }
-  long incl = sum;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const long v = __shfl_up(incl, d);
-    if (lane >= d) incl += v;
-  }
-  const long first = incl - sum;
-  const unsigned long long m = __ballot(first <= idx && idx < incl);
-  if (m == 0) return false;
-  const int src = __ffsll(m) - 1;
-  int rem = int(idx - first), e = 4 * lane, begin = 0, n = 0;
-  bool found = false;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (!found && rem < t[i]) {
-      found = true;
-      e = 4 * lane + i;
-      begin = s[i].begin;
-      n = s[i].n;
-    } else if (!found) {
-      rem -= t[i];
+    for (int i = 0; i < 4; ++i) {
+      const int e = 4 * lane + i;
+      s[i] = e < a.E ? segment_of(a, e) : Segment{0, 0};
+      t[i] = (s[i].n + tile - 1) / tile;
+      sum += t[i];
     }
+    int incl = sum;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int v = __shfl_up(incl, d);
+      if (lane >= d) incl += v;
+    }
+    first = incl - sum;
+    total = __builtin_amdgcn_readfirstlane(__shfl(incl, 63));
   }
-  auto bcast = [&](int v) { return __builtin_amdgcn_readfirstlane(__shfl(v, src)); };
-  out.e = bcast(e);
-  out.in_seg = bcast(rem);
-  out.seg_n = bcast(n);
-  out.begin = bcast(begin) + out.in_seg * tile;
-  out.n = out.seg_n - out.in_seg * tile;
-  return true;
-}
+
+  // Tile idx, 0 <= idx < total.
+  __device__ __forceinline__ RowTile at(int idx, int tile) const {
+    const int lane = threadIdx.x & 63;
+    const int src = __ffsll(__ballot(first <= idx && idx < first + sum)) - 1;
+    int rem = idx - first, e = 4 * lane, begin = 0, n = 0;
+    bool found = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (!found && rem < t[i]) {
+        found = true;
+        e = 4 * lane + i;
+        begin = s[i].begin;
+        n = s[i].n;
+      } else if (!found) {
+        rem -= t[i];
+      }
+    }
+    auto bcast = [&](int v) { return __builtin_amdgcn_readfirstlane(__shfl(v, src)); };
+    const int done = bcast(rem) * tile;
+    return RowTile{bcast(e), bcast(begin) + done, bcast(n) - done};
+  }
+};
 
 struct QuantArgs {
   const void* x;
@@ -111,6 +157,10 @@ struct CombineArgs {
   float* dweights;          // [T, k] or null
   int T, k, H, rows;
 };
+
+// Large tiles (grouped_tile.hip): which shapes they take, and their launch.
+bool grouped_tile_fits(const GroupedArgs& a, int which, int in_dt);
+hipError_t launch_grouped_tile(const GroupedArgs& a, int which, int in_dt, int out_dt, hipStream_t st);
 
 hipError_t launch_grouped(const GroupedArgs& a, int which, int in_dt, int out_dt, void* ws, hipStream_t st);
 size_t grouped_workspace(const GroupedArgs& a, int which, int in_dt, int out_dt);

@@ -48,6 +48,11 @@ bool lookup_ok(const moe_grouped_shape_t* s, const int32_t* row_ids) {
 
 moe::GroupedArgs grouped_args(const moe_grouped_shape_t* s) {
   moe::GroupedArgs a{};
+  // ceil(2^(31 + l) / row_div) with row_div <= 2^l < 2 row_div: fits 32 bits and is exact for 31-bit dividends
+  int l = 0;
+  while ((1 << l) < s->row_div) ++l;
+  a.div_mul = unsigned(((1ull << (31 + l)) + unsigned(s->row_div) - 1) / unsigned(s->row_div));
+  a.div_shift = l;
   a.rows = s->rows; a.N = s->N; a.K = s->K; a.E = s->E; a.x_rows = s->x_rows; a.row_div = s->row_div;
   return a;
 }
