@@ -11,7 +11,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SOURCES = ["csrc/api.cpp", "csrc/router.hip", "csrc/decode.hip", "csrc/decode_fused.hip", "csrc/sparse.hip",
            "csrc/prefill.hip", "csrc/probe.hip", "csrc/noalloc.hip", "csrc/cache.cpp", "csrc/operators_api.cpp",
-           "csrc/grouped.hip", "csrc/grouped_tile.hip", "csrc/rows.hip"]
+           "csrc/grouped.hip", "csrc/grouped_tile.hip", "csrc/grouped_stream.hip",
+           "csrc/rows.hip"]
 HEADERS = ["csrc/common.hpp", "csrc/router_items.hpp", "csrc/decode_items.hpp", "csrc/grouped.hpp", "../include/moe.h",
            "../include/moe_probe.h"]
 OUT = os.path.join(HERE, "lib", "libmoe.so")

@@ -15,30 +15,6 @@ namespace moe {
 
 namespace {
 
-// Up to 16 bytes from p, which need not be aligned: the first n elements (all
-// of a chunk's, or fewer at the end of a row), the others zero.
-template <class T>
-__device__ __forceinline__ u32x4_t load_chunk(const T* p, int n) {
-  constexpr int C = 16 / sizeof(T);
-  if (n >= C) {
-    struct __attribute__((packed, aligned(sizeof(T)))) U { u32x4_t v; };
-    return reinterpret_cast<const U*>(p)->v;
-  }
-  u32x4_t v = {0, 0, 0, 0};
-  if (n <= 0) return v;
-  constexpr int PW = 4 / sizeof(T);             // elements per word
-#pragma unroll
-  for (int i = 0; i < C; ++i)
-    if (i < n) {
-      uint32_t b;
-      if constexpr (sizeof(T) == 4) b = __float_as_uint(p[i]);
-      else if constexpr (sizeof(T) == 2) b = uint32_t(p[i]);
-      else b = uint32_t(uint8_t(p[i]));
-      v[i / PW] |= b << ((i % PW) * 8 * int(sizeof(T)));
-    }
-  return v;
-}
-
 // ------------------------------------------------- any size and alignment --
 // 128 x 128 tiles, four waves of 64 x 64, 128 bytes of q per stage for an
 // operand that is contiguous along q and as many rows of q otherwise.  The
@@ -240,11 +216,15 @@ hipError_t launch_any(const GroupedArgs& a, hipStream_t st) {
 
 }  // namespace
 
-size_t grouped_workspace(const GroupedArgs&, int, int, int) { return 0; }
+size_t grouped_workspace(const GroupedArgs& a, int which, int in_dt, int) {
+  return grouped_tile_workspace(a, which, in_dt);
+}
 
-hipError_t launch_grouped(const GroupedArgs& a, int which, int in_dt, int out_dt, void*, hipStream_t st) {
+hipError_t launch_grouped(const GroupedArgs& a, int which, int in_dt, int out_dt, void* ws, hipStream_t st) {
   if (which != GM_GRAD_W && a.rows == 0) return hipSuccess;
-  if (grouped_tile_fits(a, which, in_dt)) return launch_grouped_tile(a, which, in_dt, out_dt, st);
+  // few rows an expert: bound by the weights, which the stream reads at full rate
+  if (which == GM_FORWARD && long(a.rows) <= 32L * a.E) return launch_grouped_stream(a, in_dt, out_dt, st);
+  if (grouped_tile_fits(a, which, in_dt)) return launch_grouped_tile(a, which, in_dt, out_dt, ws, st);
   if (in_dt == DT_I8)
     return out_dt == DT_F32 ? launch_any<DT_I8, DT_F32, GM_FORWARD>(a, st) : launch_any<DT_I8, DT_BF16, GM_FORWARD>(a, st);
   if (which == GM_FORWARD) {

@@ -44,6 +44,33 @@ __device__ __forceinline__ void store_out(void* out, size_t i, float v) {
   else reinterpret_cast<uint16_t*>(out)[i] = uint16_t(f32_to_bf16(v));
 }
 
+// 16 bytes from p, which needs the alignment of its elements only.
+template <class T>
+__device__ __forceinline__ u32x4_t load16(const T* p) {
+  struct __attribute__((packed, aligned(sizeof(T)))) U { u32x4_t v; };
+  return reinterpret_cast<const U*>(p)->v;
+}
+// Up to 16 bytes from p, which need not be aligned: the first n elements (all
+// of a chunk's, or fewer at the end of a row), the others zero.
+template <class T>
+__device__ __forceinline__ u32x4_t load_chunk(const T* p, int n) {
+  constexpr int C = 16 / sizeof(T);
+  if (n >= C) return load16(p);
+  u32x4_t v = {0, 0, 0, 0};
+  if (n <= 0) return v;
+  constexpr int PW = 4 / sizeof(T);             // elements per word
+#pragma unroll
+  for (int i = 0; i < C; ++i)
+    if (i < n) {
+      uint32_t b;
+      if constexpr (sizeof(T) == 4) b = __float_as_uint(p[i]);
+      else if constexpr (sizeof(T) == 2) b = uint32_t(p[i]);
+      else b = uint32_t(uint8_t(p[i]));
+      v[i / PW] |= b << ((i % PW) * 8 * int(sizeof(T)));
+    }
+  return v;
+}
+
 struct GroupedArgs {
   const void* x;            // [x_rows, K] (forward, dw)
   const void* dy;           // [rows, N] (dx, dw)
@@ -54,6 +81,7 @@ struct GroupedArgs {
   const int32_t* counts;    // [E] or null
   const float* x_scale;     // 8-bit: [x_rows]
   const float* w_scale;     // 8-bit: [E, N]
+  const uint64_t* row_table;   // dw on large tiles: addresses of the rows of x in sorted order (workspace)
   int rows, N, K, E, x_rows, row_div;
   unsigned div_mul;         // n / row_div = mulhi(2 n, div_mul) >> div_shift for 0 <= n < 2^31
   int div_shift;
@@ -158,9 +186,12 @@ struct CombineArgs {
   int T, k, H, rows;
 };
 
+// Few rows an expert, forward only (grouped_stream.hip).
+hipError_t launch_grouped_stream(const GroupedArgs& a, int in_dt, int out_dt, hipStream_t st);
 // Large tiles (grouped_tile.hip): which shapes they take, and their launch.
 bool grouped_tile_fits(const GroupedArgs& a, int which, int in_dt);
-hipError_t launch_grouped_tile(const GroupedArgs& a, int which, int in_dt, int out_dt, hipStream_t st);
+size_t grouped_tile_workspace(const GroupedArgs& a, int which, int in_dt);
+hipError_t launch_grouped_tile(const GroupedArgs& a, int which, int in_dt, int out_dt, void* ws, hipStream_t st);
 
 hipError_t launch_grouped(const GroupedArgs& a, int which, int in_dt, int out_dt, void* ws, hipStream_t st);
 size_t grouped_workspace(const GroupedArgs& a, int which, int in_dt, int out_dt);

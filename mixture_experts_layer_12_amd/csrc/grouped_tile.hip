@@ -18,6 +18,8 @@
 // 16-byte chunks (32-byte pairs of them where reads transpose) are permuted
 // within each staged row so that the rows one read touches lie on distinct
 // banks.
+#include <algorithm>
+
 #include "grouped.hpp"
 
 namespace moe {
@@ -80,13 +82,13 @@ __device__ __forceinline__ const uint8_t* opaque_base(const uint8_t* p) {
   return p;
 }
 
-// One operand's loads of a wave: LOADS instructions of 1 KiB per stage (8
-// rows of 128 bytes, or 2 rows of q of 512).  Lane l of instruction i fills
-// 16 bytes of staged row `row`, chunk `chunk` of that row in memory.
-template <bool QC, int LOADS>
+// One operand's loads: instruction i of the eight waves fills 64 staged rows of
+// 128 bytes (8 a wave), or 16 rows of q of 512 bytes (2 a wave).  Lane l fills
+// 16 bytes of staged row `row`, with chunk `chunk` of that row in memory.
+template <bool QC>
 struct Share {
   __device__ __forceinline__ static int row(int wave, int i, int lane) {
-    return (wave * LOADS + i) * (QC ? 8 : 2) + (QC ? lane >> 3 : lane >> 5);
+    return (i * GT_WAVES + wave) * (QC ? 8 : 2) + (QC ? lane >> 3 : lane >> 5);
   }
   __device__ __forceinline__ static int chunk(int wave, int i, int lane) {
     const int r = row(wave, i, lane);
@@ -143,41 +145,57 @@ __device__ __forceinline__ u32x4_t read_frag(lds_byte_t* ring, uint32_t at, int 
 template <int NI>
 struct Frags { u32x4_t a[2][NI], b[2][2]; };    // [k-step parity][32-row block]
 
-// acc[i][j] += the tile's products over n_q values of q (n_q * element size a
-// multiple of 16).  `addr_a(i, t, ends)` and `addr_b` give this lane's address
-// for load i of stage t; with `ends` true_type they replace chunks past the
-// end of q by zeros.  `ahead(t)` is called well before the loads of B (t) are
-// addressed, for every t in order.
-template <int DT, bool AQ, bool BQ, int NI, class AddrA, class AddrB, class Ahead>
-__device__ __forceinline__ void tile_products(uint8_t* smem, int n_q, AddrA addr_a, AddrB addr_b, Ahead ahead,
-                                              typename Elem<DT>::acc (&acc)[NI][2]) {
+__device__ __forceinline__ uint32_t slot_a(int t) { return uint32_t(t & 1) * GT_SLOT; }
+__device__ __forceinline__ uint32_t slot_b(int t) { return uint32_t(2 + t % 3) * GT_SLOT; }
+__device__ __forceinline__ void load_to_lds(const uint8_t* from, uint8_t* to) {   // `to` + 16 bytes a lane
+  __builtin_amdgcn_global_load_lds((glb_void_t*)from, (lds_void_t*)to, 16, 0, 0);
+}
+
+// Tiles are addressed by an object `ad` with, for this lane,
+//   a(i, t, ends), b(i, t, ends)  the address of load i of stage t; with `ends`
+//             true_type chunks past the end of q are replaced by zeros
+//   ahead(t)  called well before b(.., t, ..), for every t in order
+//   n_q       values of q (n_q * element size is a multiple of 16)
+
+// The loads of stages 0 and 1 (ring slots 0 - 3): issued for the next tile
+// before the outputs of the present one, which use slot 4 only, are written.
+template <int DT, class Addr>
+__device__ __forceinline__ void first_loads(uint8_t* smem, Addr& ad, int ni) {
+  constexpr int Q = GT_STAGE / int(sizeof(typename Elem<DT>::type));
+  const int wv = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+  const int nk = (ad.n_q + Q - 1) / Q;
+  for (int t = 0; t < 2 && t < nk; ++t) {
+    ad.ahead(t);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) load_to_lds(ad.b(i, t, std::true_type{}), smem + slot_b(t) + (i * GT_WAVES + wv) * 1024);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < ni) load_to_lds(ad.a(i, t, std::true_type{}), smem + slot_a(t) + (i * GT_WAVES + wv) * 1024);
+  }
+  ad.ahead(2);
+}
+
+// acc[i][j] += the tile's products, once first_loads has been issued.
+template <int DT, bool AQ, bool BQ, int NI, class Addr>
+__device__ __forceinline__ void tile_products(uint8_t* smem, Addr& ad, typename Elem<DT>::acc (&acc)[NI][2]) {
   constexpr int Q = GT_STAGE / int(sizeof(typename Elem<DT>::type));   // values of q per stage
   const int wv = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
-  const int nk = (n_q + Q - 1) / Q, nk_full = n_q / Q;
+  const int nk = (ad.n_q + Q - 1) / Q, nk_full = ad.n_q / Q;
   lds_byte_t* const ring = (lds_byte_t*)smem;
   const uint32_t off_a = frag_offset<AQ>((wv >> 2) * 32 * NI), off_b = frag_offset<BQ>((wv & 3) * 64);
-  auto slot_a = [](int t) { return uint32_t(t & 1) * GT_SLOT; };
-  auto slot_b = [](int t) { return uint32_t(2 + t % 3) * GT_SLOT; };
 
   auto load_a = [&](int t, auto i0, auto i1, auto ends) {
-    for_range<decltype(i0)::value, decltype(i1)::value>([&](auto ic) {
-      constexpr int i = decltype(ic)::value;
-      __builtin_amdgcn_global_load_lds((glb_void_t*)addr_a(i, t, ends),
-                                       (lds_void_t*)(smem + slot_a(t) + (wv * NI + i) * 1024), 16, 0, 0);
-    });
+    for_range<decltype(i0)::value, decltype(i1)::value>(
+        [&](auto ic) { load_to_lds(ad.a(int(ic), t, ends), smem + slot_a(t) + (int(ic) * GT_WAVES + wv) * 1024); });
   };
   auto load_b = [&](int t, auto i0, auto i1, auto ends) {
-    for_range<decltype(i0)::value, decltype(i1)::value>([&](auto ic) {
-      constexpr int i = decltype(ic)::value;
-      __builtin_amdgcn_global_load_lds((glb_void_t*)addr_b(i, t, ends),
-                                       (lds_void_t*)(smem + slot_b(t) + (wv * 4 + i) * 1024), 16, 0, 0);
-    });
+    for_range<decltype(i0)::value, decltype(i1)::value>(
+        [&](auto ic) { load_to_lds(ad.b(int(ic), t, ends), smem + slot_b(t) + (int(ic) * GT_WAVES + wv) * 1024); });
   };
   using I0 = std::integral_constant<int, 0>;
   using I2 = std::integral_constant<int, 2>;
   using I4 = std::integral_constant<int, 4>;
   using IA = std::integral_constant<int, NI>;
-  using IA2 = std::integral_constant<int, (NI + 1) / 2>;
   using Yes = std::true_type;
   using No = std::false_type;
 
@@ -226,7 +244,7 @@ __device__ __forceinline__ void tile_products(uint8_t* smem, int n_q, AddrA addr
     wait_loads<4>();            // all but B (t + 2): stage t + 1 has landed (this wave's part)
     stage_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    ahead(t + 3);
+    ad.ahead(t + 3);
     step(1, opaque(slot_a(t + 1) + off_a), opaque(slot_b(t + 1) + off_b), 0, IA{}, [&](auto i) { one_a(t + 2, i); });
   };
   // The same with the ends checked (the last stages, short reductions).
@@ -245,7 +263,7 @@ __device__ __forceinline__ void tile_products(uint8_t* smem, int n_q, AddrA addr
       else wait_loads<0>();
       stage_barrier();
     }
-    ahead(t + 3);
+    ad.ahead(t + 3);
     multiply(1);
     if (more) {
       read_step(slot_a(t + 1) + off_a, slot_b(t + 1) + off_b, 0);
@@ -254,18 +272,7 @@ __device__ __forceinline__ void tile_products(uint8_t* smem, int n_q, AddrA addr
   };
 
   if (nk == 0) return;
-  ahead(0);
-  load_a(0, I0{}, IA{}, Yes{});
-  load_b(0, I0{}, I4{}, Yes{});
-  if (nk > 1) {
-    ahead(1);
-    load_b(1, I0{}, I4{}, Yes{});
-    load_a(1, I0{}, IA{}, Yes{});
-    ahead(2);
-    wait_loads<4 + NI>();
-  } else {
-    wait_loads<0>();
-  }
+  wait_loads<0>();              // stages 0 and 1 (and the stores of the tile before)
   stage_barrier();
   read_step(slot_a(0) + off_a, slot_b(0) + off_b, 0);
   int t = 0;
@@ -276,17 +283,21 @@ __device__ __forceinline__ void tile_products(uint8_t* smem, int n_q, AddrA addr
 // Writes a wave's 32 NI x 64 part of a tile: rows from `row` (those below
 // `end`), columns from `col` (below n_cols) of the row-major `out`.  `value(x,
 // r, s)` makes the output of sum x in row r of the tile, s = `col_scale(n)`.
-// The sums go through LDS, 32 rows at a time, so that a store instruction
-// covers whole 128-byte lines (stored as they lie in registers, 64-byte pieces
-// of bf16, the epilogue took longer than 8 stages of the main loop).  Rows of
-// out that are not 16-byte aligned are stored element by element.
-constexpr int GT_OUT_ROW = 64 * 4 + 16;           // bytes of a staged row: 64 columns, and a pad for the banks
-constexpr int GT_OUT_WAVE = 32 * GT_OUT_ROW;
+// The sums go through LDS, 16 rows of bf16 or 8 of fp32 at a time, so that a
+// store instruction covers whole 128-byte lines (stored as they lie in
+// registers, in 64-byte pieces of bf16, the outputs of a tile took longer than
+// 4 stages of the main loop).  Rows of out that are not 16-byte aligned are
+// stored element by element.  `mine`: the wave's GT_OUT_WAVE bytes.
+constexpr int GT_OUT_WAVE = 16 * (64 * 2 + 16);   // rows padded by 16 bytes for the banks
+static_assert(8 * (64 * 4 + 16) <= GT_OUT_WAVE, "8 rows of fp32");
+constexpr int GT_OUT = 4 * GT_SLOT;               // the waves' areas start at slot 4; then 256 row scales
+static_assert(GT_WAVES * GT_OUT_WAVE + 256 * 4 <= GT_SLOT, "one slot");
 template <int OUT, int NI, class Acc, class Value, class Scale>
-__device__ __forceinline__ void store_tile(uint8_t* smem, const Acc (&acc)[NI][2], void* out, int tile_row, int row,
+__device__ __forceinline__ void store_tile(uint8_t* mine, const Acc (&acc)[NI][2], void* out, int tile_row, int row,
                                            int end, int col, int n_cols, Scale col_scale, Value value) {
   constexpr int B = OUT == DT_F32 ? 4 : 2, C = 16 / B;
   constexpr int LPR = 64 / C, RPI = 64 / LPR;     // lanes per row and rows per store instruction
+  constexpr int CR = OUT == DT_F32 ? 8 : 16, ROW = 64 * B + 16;   // rows staged at a time, bytes of one
   const int lane = lane_here(), l32 = lane & 31, hi = lane >> 5;
   // register q of lane l: row 8 (q / 4) + 4 (l / 32) + q % 4 of a 32 x 32 block, column l % 32
   float s[2];
@@ -307,33 +318,41 @@ __device__ __forceinline__ void store_tile(uint8_t* smem, const Acc (&acc)[NI][2
     }
     return;
   }
-  uint8_t* const mine = smem + __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6)) * GT_OUT_WAVE;
   const int cr = lane / LPR, cc = (lane % LPR) * C;
 #pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    if (row + 32 * i >= end) return;
+  for (int i = 0; i < NI; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int h = 0; h < 32 / CR; ++h) {
+      const int first = 32 * i + CR * h;
+      if (row + first >= end) return;
 #pragma unroll
-      for (int q = 0; q < 16; ++q) {
-        const int r = 8 * (q >> 2) + 4 * hi + (q & 3);
-        const float v = value(acc[i][j][q], tile_row + 32 * i + r, s[j]);
-        uint8_t* p = mine + r * GT_OUT_ROW + (32 * j + l32) * B;
-        if constexpr (OUT == DT_F32) *reinterpret_cast<float*>(p) = v;
-        else *reinterpret_cast<uint16_t*>(p) = uint16_t(f32_to_bf16(v));
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int q = h * CR / 2; q < (h + 1) * CR / 2; ++q) {
+          const int r = 8 * (q >> 2) + 4 * hi + (q & 3);
+          const float v = value(acc[i][j][q], tile_row + 32 * i + r, s[j]);
+          uint8_t* p = mine + (r - CR * h) * ROW + (32 * j + l32) * B;
+          if constexpr (OUT == DT_F32) *reinterpret_cast<float*>(p) = v;
+          else *reinterpret_cast<uint16_t*>(p) = uint16_t(f32_to_bf16(v));
+        }
+      // LDS serves a wave's accesses in order; the compiler has to keep it
+      asm volatile("" ::: "memory");
+#pragma unroll
+      for (int k = 0; k < CR / RPI; ++k) {
+        const int r = k * RPI + cr;
+        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(mine + r * ROW + cc * B);
+        if (row + first + r < end && col + cc < n_cols)
+          *reinterpret_cast<u32x4_t*>(reinterpret_cast<uint8_t*>(out) +
+                                      (size_t(row + first + r) * n_cols + col + cc) * B) = v;
       }
-    // LDS serves a wave's accesses in order; the compiler has to keep it
-    asm volatile("" ::: "memory");
-#pragma unroll
-    for (int k = 0; k < 32 / RPI; ++k) {
-      const int r = k * RPI + cr;
-      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(mine + r * GT_OUT_ROW + cc * B);
-      if (row + 32 * i + r < end && col + cc < n_cols)
-        *reinterpret_cast<u32x4_t*>(reinterpret_cast<uint8_t*>(out) + (size_t(row + 32 * i + r) * n_cols + col + cc) * B) = v;
+      asm volatile("" ::: "memory");
     }
-    asm volatile("" ::: "memory");
-  }
 }
+
+// A resident work-group (one per CU: the ring is all of its LDS) takes its
+// items one after another, and while the outputs of one are written the first
+// loads of the next are under way.
+constexpr int GT_GRID = 256;
 
 // ------------------------------------------------------- forward and dx --
 // Item list: (column group, row tile, column) over the row tiles that the
@@ -343,61 +362,96 @@ __device__ __forceinline__ void store_tile(uint8_t* smem, const Acc (&acc)[NI][2
 // takes one contiguous eighth.
 constexpr int GT_CG = 4;
 
-// One tile: `rows` sorted rows from row0 (at most 64 NI), columns from n0.
-template <int DT, int OUT, int WHICH, int NI>
-__device__ __forceinline__ void rows_tile(const GroupedArgs& a, uint8_t* smem, int e, int row0, int rows, int n0) {
-  typedef typename Elem<DT>::type T;
-  constexpr int C = 16 / int(sizeof(T));
-  constexpr bool BQ = WHICH == GM_FORWARD;
-  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
-  const int n_cols = WHICH == GM_FORWARD ? a.N : a.K, n_q = WHICH == GM_FORWARD ? a.K : a.N;
-  const uint8_t* const zeros = reinterpret_cast<const uint8_t*>(&g_zeros);
-  const T* const w = reinterpret_cast<const T*>(a.w) + size_t(e) * a.N * a.K;
+struct RowsItem {
+  int e, row0, rows, n0;       // expert, first sorted row, rows (at most 256; 0: there is no item), first column
+  __device__ __forceinline__ int blocks() const { return rows > 128 ? 4 : (rows > 64 ? 2 : 1); }   // NI
+};
 
-  // Rows without a source, and rows past the segment, load some row that exists (w's first, or the tile's
-  // first of dy): their products are replaced or not stored.  Likewise the columns past the last.  Rows
-  // found through row_ids may lie anywhere in x; all else is within 2^32 bytes of the tile's first row.
-  typedef Share<true, NI> SA;
-  typedef Share<BQ, 4> SB;
-  const uint8_t* pa[NI];
-  uint32_t oa[NI], ob[4];
-  const uint8_t* const dy0 = reinterpret_cast<const uint8_t*>(reinterpret_cast<const T*>(a.dy) + size_t(row0) * a.N);
-  const uint8_t* const w0 = reinterpret_cast<const uint8_t*>(w + (BQ ? size_t(n0) * a.K : size_t(n0)));
+template <int WHICH>
+__device__ __forceinline__ RowsItem rows_item(const GroupedArgs& a, long it) {
+  const int n_ct = ((WHICH == GM_FORWARD ? a.N : a.K) + GT_N - 1) / GT_N, xcd = blockIdx.x & 7;
+  const RowTiles tiles(a, 256);
+  const long n_items = long(tiles.total) * n_ct;
+  const long item = xcd * n_items / 8 + it;
+  if (item >= (xcd + 1) * n_items / 8) return RowsItem{0, 0, 0, 0};
+  const long per_group = long(tiles.total) * GT_CG;
+  const int g = int(item / per_group), in_g = int(item - g * per_group);
+  const int width = min(GT_CG, n_ct - g * GT_CG);
+  const RowTile rt = tiles.at(in_g / width, 256);
+  return RowsItem{rt.e, rt.begin, min(rt.n, 256), __builtin_amdgcn_readfirstlane((g * GT_CG + in_g % width) * GT_N)};
+}
+
+// Addresses of one tile.  Rows without a source, and rows past the segment,
+// load some row that exists (w's first, or the tile's first of dy): their
+// products are replaced or not stored.  Likewise the columns past the last.
+// Rows found through row_ids may lie anywhere in x; all else is within 2^32
+// bytes of the tile's first row.
+template <int DT, int WHICH>
+struct RowsAddr {
+  typedef typename Elem<DT>::type T;
+  static constexpr bool BQ = WHICH == GM_FORWARD;
+  static constexpr int C = 16 / int(sizeof(T));
+  const uint8_t* pa[WHICH == GM_FORWARD ? 4 : 1];
+  uint32_t oa[4], ob[4];
+  const uint8_t *dy0, *w0;
+  size_t row_bytes, step_b;
+  int n_q, wv;
+
+  __device__ __forceinline__ void set(const GroupedArgs& a, const RowsItem& it) {
+    const int lane = threadIdx.x & 63;
+    wv = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+    const int n_cols = WHICH == GM_FORWARD ? a.N : a.K;
+    n_q = WHICH == GM_FORWARD ? a.K : a.N;
+    row_bytes = size_t(n_q) * sizeof(T);
+    step_b = BQ ? GT_STAGE : size_t(64) * a.K * sizeof(T);
+    const T* const w = reinterpret_cast<const T*>(a.w) + size_t(it.e) * a.N * a.K;
+    w0 = reinterpret_cast<const uint8_t*>(w + (BQ ? size_t(it.n0) * a.K : size_t(it.n0)));
+    dy0 = reinterpret_cast<const uint8_t*>(reinterpret_cast<const T*>(a.dy) + size_t(it.row0) * a.N);
 #pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    const int r = SA::row(wv, i, lane), c = SA::chunk(wv, i, lane) * 16;
-    if constexpr (WHICH == GM_FORWARD) {
-      const int src = r < rows ? source_row(a, row0 + r) : -1;
-      pa[i] = reinterpret_cast<const uint8_t*>(src < 0 ? w : reinterpret_cast<const T*>(a.x) + size_t(src) * a.K) + c;
-    } else {
-      oa[i] = uint32_t(r < rows ? r : 0) * uint32_t(a.N * int(sizeof(T))) + c;
+    for (int i = 0; i < 4; ++i) {
+      const int r = Share<true>::row(wv, i, lane), c = Share<true>::chunk(wv, i, lane) * 16;
+      if constexpr (WHICH == GM_FORWARD) {
+        const int src = r < it.rows ? source_row(a, it.row0 + r) : -1;
+        pa[i] = reinterpret_cast<const uint8_t*>(src < 0 ? w : reinterpret_cast<const T*>(a.x) + size_t(src) * a.K) + c;
+      } else {
+        oa[i] = uint32_t(r < it.rows ? r : 0) * uint32_t(a.N * int(sizeof(T))) + c;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = Share<BQ>::row(wv, i, lane), c = Share<BQ>::chunk(wv, i, lane) * C;
+      if constexpr (BQ) ob[i] = (uint32_t(it.n0 + r < n_cols ? r : 0) * uint32_t(a.K) + c) * uint32_t(sizeof(T));
+      else ob[i] = (uint32_t(r) * uint32_t(a.K) + (it.n0 + c < n_cols ? c : 0)) * uint32_t(sizeof(T));
     }
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = SB::row(wv, i, lane), c = SB::chunk(wv, i, lane) * C;
-    if constexpr (BQ) ob[i] = (uint32_t(n0 + r < n_cols ? r : 0) * uint32_t(a.K) + c) * uint32_t(sizeof(T));
-    else ob[i] = (uint32_t(r) * uint32_t(a.K) + (n0 + c < n_cols ? c : 0)) * uint32_t(sizeof(T));
-  }
-  const size_t row_bytes = size_t(n_q) * sizeof(T);
-  const size_t step_b = BQ ? GT_STAGE : size_t(64) * a.K * sizeof(T);
-  auto addr_a = [&](int i, int t, auto ends) {
+  template <class Ends>
+  __device__ __forceinline__ const uint8_t* a(int i, int t, Ends) const {
     const uint8_t* p;
     if constexpr (WHICH == GM_FORWARD) p = pa[i] + size_t(t) * GT_STAGE;
     else p = opaque_base(dy0 + size_t(t) * GT_STAGE) + oa[i];
-    if constexpr (decltype(ends)::value)
-      if (size_t(t) * GT_STAGE + SA::chunk(wv, i, lane_here()) * 16 >= row_bytes) p = zeros;
+    if constexpr (Ends::value)
+      if (size_t(t) * GT_STAGE + Share<true>::chunk(wv, i, lane_here()) * 16 >= row_bytes)
+        p = reinterpret_cast<const uint8_t*>(&g_zeros);
     return p;
-  };
-  auto addr_b = [&](int i, int t, auto ends) {
+  }
+  template <class Ends>
+  __device__ __forceinline__ const uint8_t* b(int i, int t, Ends) const {
     const uint8_t* p = opaque_base(w0 + size_t(t) * step_b) + ob[i];
-    if constexpr (decltype(ends)::value)
-      if (BQ ? size_t(t) * GT_STAGE + SB::chunk(wv, i, lane_here()) * 16 >= row_bytes
-             : t * 64 + SB::row(wv, i, lane_here()) >= n_q)
-        p = zeros;
+    if constexpr (Ends::value)
+      if (BQ ? size_t(t) * GT_STAGE + Share<true>::chunk(wv, i, lane_here()) * 16 >= row_bytes
+             : t * 64 + Share<false>::row(wv, i, lane_here()) >= n_q)
+        p = reinterpret_cast<const uint8_t*>(&g_zeros);
     return p;
-  };
+  }
+  __device__ __forceinline__ void ahead(int) {}
+};
 
+// The products and outputs of tile `cur`; between them the first loads of `next`.
+template <int DT, int OUT, int WHICH, int NI>
+__device__ __forceinline__ void rows_tile(const GroupedArgs& a, uint8_t* smem, RowsAddr<DT, WHICH>& ad,
+                                          const RowsItem& cur, const RowsItem& next, float scale) {
+  const int wv = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+  const int n_cols = WHICH == GM_FORWARD ? a.N : a.K;
   typename Elem<DT>::acc acc[NI][2];
 #pragma unroll
   for (int i = 0; i < NI; ++i)
@@ -405,23 +459,20 @@ __device__ __forceinline__ void rows_tile(const GroupedArgs& a, uint8_t* smem, i
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int q = 0; q < 16; ++q) acc[i][j][q] = 0;
-  tile_products<DT, true, BQ, NI>(smem, n_q, addr_a, addr_b, [](int) {}, acc);
+  tile_products<DT, true, WHICH == GM_FORWARD, NI>(smem, ad, acc);
 
-  // The rows' scales (8-bit), or 1; 0 for a row that stands for zeros.
-  float* const row_scale = reinterpret_cast<float*>(smem + GT_WAVES * GT_OUT_WAVE);
-  __syncthreads();
-  if constexpr (WHICH == GM_FORWARD) {
-    if (int(threadIdx.x) < 64 * NI) {
-      const int r = threadIdx.x;
-      const int src = r < rows ? source_row(a, row0 + r) : -1;
-      row_scale[r] = src < 0 ? 0.f : (DT == DT_I8 ? a.x_scale[src] : 1.f);
-    }
-    __syncthreads();
+  stage_barrier();                               // every wave is through with the ring
+  float* const row_scale = reinterpret_cast<float*>(smem + GT_OUT + GT_WAVES * GT_OUT_WAVE);
+  if (WHICH == GM_FORWARD && threadIdx.x < 256) row_scale[threadIdx.x] = scale;
+  if (next.rows) {
+    ad.set(a, next);
+    first_loads<DT>(smem, ad, next.blocks());
   }
+  stage_barrier();
   const int m0 = (wv >> 2) * 32 * NI;
   store_tile<OUT, NI>(
-      smem, acc, a.out, m0, row0 + m0, row0 + rows, n0 + (wv & 3) * 64, n_cols,
-      [&](int n) { return DT == DT_I8 ? a.w_scale[size_t(e) * a.N + n] : 0.f; },
+      smem + GT_OUT + wv * GT_OUT_WAVE, acc, a.out, m0, cur.row0 + m0, cur.row0 + cur.rows, cur.n0 + (wv & 3) * 64, n_cols,
+      [&](int n) { return DT == DT_I8 ? a.w_scale[size_t(cur.e) * a.N + n] : 0.f; },
       [&](auto x, int r, float ws) {
         if constexpr (DT == DT_I8) return float(x) * row_scale[r] * ws;
         else return WHICH == GM_FORWARD && row_scale[r] == 0.f ? 0.f : float(x);
@@ -431,35 +482,36 @@ __device__ __forceinline__ void rows_tile(const GroupedArgs& a, uint8_t* smem, i
 template <int DT, int OUT, int WHICH>
 __global__ void __launch_bounds__(64 * GT_WAVES) grouped_rows_kernel(GroupedArgs a) {
   __shared__ __attribute__((aligned(16))) uint8_t smem[GT_LDS];
-  constexpr int TM = 256;
-  const int n_cols = WHICH == GM_FORWARD ? a.N : a.K;
-  const int n_ct = (n_cols + GT_N - 1) / GT_N;
-  const int xcd = blockIdx.x & 7;
-  for (long it = blockIdx.x >> 3;; it += gridDim.x >> 3) {
-    const RowTiles tiles(a, TM);                 // looked up anew per item: kept, it would cost registers below
-    const long n_items = long(tiles.total) * n_ct;
-    const long item = xcd * n_items / 8 + it;
-    if (item >= (xcd + 1) * n_items / 8) return;
-    const long per_group = long(tiles.total) * GT_CG;
-    const int g = int(item / per_group);
-    const int in_g = int(item - g * per_group);
-    const int width = min(GT_CG, n_ct - g * GT_CG);
-    const int n0 = (g * GT_CG + in_g % width) * GT_N;
-    const RowTile rt = tiles.at(in_g / width, TM);
+  long it = blockIdx.x >> 3;
+  RowsItem cur = rows_item<WHICH>(a, it);
+  if (!cur.rows) return;
+  RowsAddr<DT, WHICH> ad;
+  ad.set(a, cur);
+  first_loads<DT>(smem, ad, cur.blocks());
+  while (true) {
+    // the row's scale (8-bit), or 1; 0 for a row that stands for zeros
+    float scale = 0.f;
+    if (WHICH == GM_FORWARD && int(threadIdx.x) < cur.rows) {
+      const int src = source_row(a, cur.row0 + int(threadIdx.x));
+      scale = src < 0 ? 0.f : (DT == DT_I8 ? a.x_scale[src] : 1.f);
+    }
+    it += gridDim.x >> 3;
+    const RowsItem next = rows_item<WHICH>(a, it);
     // the last rows of a segment take the smallest tile that holds them
-    if (rt.n > 128) rows_tile<DT, OUT, WHICH, 4>(a, smem, rt.e, rt.begin, min(rt.n, TM), n0);
-    else if (rt.n > 64) rows_tile<DT, OUT, WHICH, 2>(a, smem, rt.e, rt.begin, rt.n, n0);
-    else rows_tile<DT, OUT, WHICH, 1>(a, smem, rt.e, rt.begin, rt.n, n0);
-    __syncthreads();                             // the ring is free for the next item
+    if (cur.rows > 128) rows_tile<DT, OUT, WHICH, 4>(a, smem, ad, cur, next, scale);
+    else if (cur.rows > 64) rows_tile<DT, OUT, WHICH, 2>(a, smem, ad, cur, next, scale);
+    else rows_tile<DT, OUT, WHICH, 1>(a, smem, ad, cur, next, scale);
+    if (!next.rows) return;
+    cur = next;
   }
 }
 
 template <int DT, int OUT, int WHICH>
 hipError_t launch_rows(const GroupedArgs& a, hipStream_t st) {
   const long n_ct = ((WHICH == GM_FORWARD ? a.N : a.K) + GT_N - 1) / GT_N;
-  const long n_items = (long(a.rows) / 256 + a.E) * n_ct;       // every segment may end in a part of a tile
-  const long grid = (n_items < (1L << 20) ? n_items : (1L << 20)) + 7;
-  hipLaunchKernelGGL((grouped_rows_kernel<DT, OUT, WHICH>), dim3(unsigned(grid / 8 * 8)), dim3(64 * GT_WAVES), 0, st, a);
+  const long n_items = (long(a.rows) / 256 + (a.E < a.rows ? a.E : a.rows)) * n_ct;   // segments may end in part of a tile
+  const long grid = n_items < GT_GRID ? (n_items + 7) / 8 * 8 : GT_GRID;
+  hipLaunchKernelGGL((grouped_rows_kernel<DT, OUT, WHICH>), dim3(unsigned(grid)), dim3(64 * GT_WAVES), 0, st, a);
   return hipGetLastError();
 }
 
@@ -467,77 +519,111 @@ hipError_t launch_rows(const GroupedArgs& a, hipStream_t st) {
 // One item per 256 x 256 tile of dw[e]; the reduction runs over e's rows.
 // Experts' work differs with their rows, so each XCD takes an eighth of every
 // expert's tiles, in order (they share panels of dy and x in that XCD's L2).
-// LOOKUP: the rows of x are found through row_ids, which are read one stage
-// before the loads that they address.
+struct DwItem {
+  int e, m0, n0, begin, n;     // expert (-1: there is no item), tile of dw[e], e's segment
+};
+
+__device__ __forceinline__ DwItem dw_item(const GroupedArgs& a, long& it) {
+  const int n_nt = (a.K + GT_N - 1) / GT_N;
+  const long per_expert = long((a.N + 255) / 256) * n_nt, share = (per_expert + 7) / 8;
+  for (; it < share * a.E; it += gridDim.x >> 3) {
+    const long tile = long(blockIdx.x & 7) * share + it % share;
+    if (tile >= per_expert) continue;
+    const int e = int(it / share);
+    const Segment s = segment_of(a, e);
+    auto uni = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+    return DwItem{uni(e), uni(int(tile / n_nt) * 256), uni(int(tile % n_nt) * GT_N), uni(s.begin), uni(s.n)};
+  }
+  return DwItem{-1, 0, 0, 0, 0};
+}
+
+// LOOKUP: the rows of x are found through a table of their addresses (8 bytes
+// a sorted row, see row_table_kernel).  Each load fills two rows of q, so a
+// wave's rows of a stage are eight table entries that all its lanes share:
+// scalar loads, a stage ahead, which do not count among the vector loads that
+// the stages wait for.
+template <bool LOOKUP>
+struct DwAddr {
+  uint32_t oa[4], ob[4];
+  const uint8_t *dy0, *x0;
+  size_t step_a, step_b;
+  int n_q, wv, last;
+  const uint64_t* table;
+  uint64_t at[8];
+
+  __device__ __forceinline__ void set(const GroupedArgs& a, const DwItem& it) {
+    const int lane = threadIdx.x & 63;
+    wv = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+    n_q = it.n;
+    last = (it.n + 63) / 64 - 1;
+    step_a = size_t(64) * a.N * 2;
+    step_b = size_t(64) * a.K * 2;
+    dy0 = reinterpret_cast<const uint8_t*>(reinterpret_cast<const uint16_t*>(a.dy) + size_t(it.begin) * a.N + it.m0);
+    x0 = reinterpret_cast<const uint8_t*>(reinterpret_cast<const uint16_t*>(a.x) + size_t(it.begin) * a.K + it.n0);
+    table = a.row_table + it.begin + wv * 2;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      // columns past the last read the tile's first ones: their products are not stored
+      const int r = Share<false>::row(wv, i, lane), c = Share<false>::chunk(wv, i, lane) * 8;
+      oa[i] = (uint32_t(r) * uint32_t(a.N) + (it.m0 + c < a.N ? c : 0)) * 2u;
+      const uint32_t col = it.n0 + c < a.K ? c : 0;
+      ob[i] = LOOKUP ? (it.n0 + col) * 2u : (uint32_t(r) * uint32_t(a.K) + col) * 2u;
+    }
+  }
+  template <class Ends>
+  __device__ __forceinline__ const uint8_t* a(int i, int t, Ends) const {
+    const uint8_t* p = opaque_base(dy0 + size_t(t) * step_a) + oa[i];
+    if constexpr (Ends::value)
+      if (t * 64 + Share<false>::row(wv, i, lane_here()) >= n_q) p = reinterpret_cast<const uint8_t*>(&g_zeros);
+    return p;
+  }
+  template <class Ends>
+  __device__ __forceinline__ const uint8_t* b(int i, int t, Ends) const {
+    const uint8_t* p;
+    if constexpr (LOOKUP) p = reinterpret_cast<const uint8_t*>((threadIdx.x & 32) ? at[2 * i + 1] : at[2 * i]) + ob[i];
+    else p = opaque_base(x0 + size_t(t) * step_b) + ob[i];
+    if constexpr (Ends::value)
+      if (t * 64 + Share<false>::row(wv, i, lane_here()) >= n_q) p = reinterpret_cast<const uint8_t*>(&g_zeros);
+    return p;
+  }
+  __device__ __forceinline__ void ahead(int t) {
+    if constexpr (LOOKUP) {
+      typedef const __attribute__((address_space(4))) uint64_t const_u64_t;
+      const_u64_t* const p = (const_u64_t*)(table) + max(min(t, last), 0) * 64;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) at[2 * i] = p[16 * i], at[2 * i + 1] = p[16 * i + 1];
+    }
+  }
+};
+
+// Table of the addresses of the rows of x in sorted order, and a row of zeros
+// behind it for rows without a source.  Entries past the last row (a stage
+// reads whole blocks of 64) name the row of zeros as well.
+constexpr int GT_TABLE_PAD = 64;
+__host__ __device__ inline long zero_row_entry(const GroupedArgs& a) { return (long(a.rows) + GT_TABLE_PAD + 1) / 2 * 2; }
+__global__ void __launch_bounds__(256) row_table_kernel(GroupedArgs a, uint64_t* table, uint16_t* zero_row) {
+  const long i = long(blockIdx.x) * 256 + threadIdx.x;
+  if (i < zero_row_entry(a)) {
+    const int src = i < a.rows ? source_row(a, int(i)) : -1;
+    const uint16_t* p = src < 0 ? zero_row : reinterpret_cast<const uint16_t*>(a.x) + size_t(src) * a.K;
+    table[i] = reinterpret_cast<uint64_t>(p);
+  }
+  if (i < a.K) zero_row[i] = 0;
+}
+
 template <int OUT, bool LOOKUP>
 __global__ void __launch_bounds__(64 * GT_WAVES) grouped_dw_kernel(GroupedArgs a) {
   __shared__ __attribute__((aligned(16))) uint8_t smem[GT_LDS];
-  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
-  const int n_mt = (a.N + 255) / 256, n_nt = (a.K + GT_N - 1) / GT_N;
-  const long per_expert = long(n_mt) * n_nt, share = (per_expert + 7) / 8;
-  const uint8_t* const zeros = reinterpret_cast<const uint8_t*>(&g_zeros);
-
-  for (long it = blockIdx.x >> 3; it < share * a.E; it += gridDim.x >> 3) {
-    const int e = __builtin_amdgcn_readfirstlane(int(it / share));
-    const long tile = long(blockIdx.x & 7) * share + it % share;
-    if (tile >= per_expert) continue;
-    const int m0 = __builtin_amdgcn_readfirstlane(int(tile / n_nt)) * 256;
-    const int n0 = __builtin_amdgcn_readfirstlane(int(tile % n_nt)) * GT_N;
-    Segment seg = segment_of(a, e);
-    seg.begin = __builtin_amdgcn_readfirstlane(seg.begin);
-    const int n_q = __builtin_amdgcn_readfirstlane(seg.n);
-
-    typedef Share<false, 4> S;
-    // Each load fills two rows of q, so the wave's rows of a stage are eight entries of row_ids that all its
-    // lanes share: scalar loads, which do not count among the vector loads that the stages wait for.
-    int id[8];
-    typedef const __attribute__((address_space(4))) int32_t const_i32_t;
-    const_i32_t* const ids = (const_i32_t*)(a.row_ids);
-    auto ahead = [&](int t) {
-      if constexpr (LOOKUP) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) id[i] = ids[seg.begin + max(min(t * 64 + wv * 8 + i, n_q - 1), 0)];
-      }
-    };
-    // columns past the last read the tile's first ones: their products are not stored
-    const uint8_t* const dy0 = reinterpret_cast<const uint8_t*>(reinterpret_cast<const uint16_t*>(a.dy) +
-                                                                size_t(seg.begin) * a.N + m0);
-    const uint8_t* const x0 = reinterpret_cast<const uint8_t*>(reinterpret_cast<const uint16_t*>(a.x) +
-                                                               (LOOKUP ? 0 : size_t(seg.begin) * a.K) + n0);
-    uint32_t oa[4], ob[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = S::row(wv, i, lane), c = S::chunk(wv, i, lane) * 8;
-      oa[i] = (uint32_t(r) * uint32_t(a.N) + (m0 + c < a.N ? c : 0)) * 2u;
-      ob[i] = ((LOOKUP ? 0u : uint32_t(r) * uint32_t(a.K)) + (n0 + c < a.K ? c : 0)) * 2u;
-    }
-    const size_t step_a = size_t(64) * a.N * 2, step_b = size_t(64) * a.K * 2;
-    auto addr_a = [&](int i, int t, auto ends) {
-      const uint8_t* p = opaque_base(dy0 + size_t(t) * step_a) + oa[i];
-      if constexpr (decltype(ends)::value)
-        if (t * 64 + S::row(wv, i, lane_here()) >= n_q) p = zeros;
-      return p;
-    };
-    auto addr_b = [&](int i, int t, auto ends) {
-      const uint8_t* p;
-      if constexpr (LOOKUP) {
-        // selects between values that are there either way: no branches in the main loop
-        const int s0 = source_of(a, id[2 * i]), s1 = source_of(a, id[2 * i + 1]);
-        const uint64_t row = uint64_t(a.K) * 2u;
-        const uint64_t r0 = uint64_t(x0) + uint64_t(unsigned(max(s0, 0))) * row;
-        const uint64_t r1 = uint64_t(x0) + uint64_t(unsigned(max(s1, 0))) * row;
-        const uint64_t p0 = s0 < 0 ? uint64_t(zeros) : r0, p1 = s1 < 0 ? uint64_t(zeros) : r1;
-        const uint32_t o0 = s0 < 0 ? 0u : ob[i], o1 = s1 < 0 ? 0u : ob[i];
-        const bool second = lane >= 32;
-        p = reinterpret_cast<const uint8_t*>((second ? p1 : p0) + (second ? o1 : o0));
-      } else {
-        p = opaque_base(x0 + size_t(t) * step_b) + ob[i];
-      }
-      if constexpr (decltype(ends)::value)
-        if (t * 64 + S::row(wv, i, lane_here()) >= n_q) p = zeros;
-      return p;
-    };
-
+  const int wv = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+  long it = blockIdx.x >> 3;
+  DwItem cur = dw_item(a, it);
+  if (cur.e < 0) return;
+  DwAddr<LOOKUP> ad;
+  ad.set(a, cur);
+  first_loads<DT_BF16>(smem, ad, 4);
+  while (true) {
+    it += gridDim.x >> 3;
+    const DwItem next = dw_item(a, it);
     f32x16_t acc[4][2];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -545,26 +631,39 @@ __global__ void __launch_bounds__(64 * GT_WAVES) grouped_dw_kernel(GroupedArgs a
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
-    tile_products<DT_BF16, false, false, 4>(smem, n_q, addr_a, addr_b, ahead, acc);
-
-    __syncthreads();
-    const int m = m0 + (wv >> 2) * 128;
+    tile_products<DT_BF16, false, false, 4>(smem, ad, acc);
+    stage_barrier();                             // every wave is through with the ring
+    if (next.e >= 0) {
+      ad.set(a, next);
+      first_loads<DT_BF16>(smem, ad, 4);
+    }
+    const int m = cur.m0 + (wv >> 2) * 128;
     store_tile<OUT, 4>(
-        smem, acc, reinterpret_cast<uint8_t*>(a.out) + size_t(e) * a.N * a.K * (OUT == DT_F32 ? 4 : 2), 0, m, a.N,
-        n0 + (wv & 3) * 64, a.K, [](int) { return 0.f; }, [](float x, int, float) { return x; });
-    __syncthreads();
+        smem + GT_OUT + wv * GT_OUT_WAVE, acc,
+        reinterpret_cast<uint8_t*>(a.out) + size_t(cur.e) * a.N * a.K * (OUT == DT_F32 ? 4 : 2), 0, m, a.N,
+        cur.n0 + (wv & 3) * 64, a.K, [](int) { return 0.f; }, [](float x, int, float) { return x; });
+    if (next.e < 0) return;
+    cur = next;
   }
 }
 
 template <int OUT>
-hipError_t launch_dw(const GroupedArgs& a, hipStream_t st) {
+hipError_t launch_dw(const GroupedArgs& args, void* ws, hipStream_t st) {
+  GroupedArgs a = args;
   const long per_expert = long((a.N + 255) / 256) * ((a.K + GT_N - 1) / GT_N);
   const long n_items = (per_expert + 7) / 8 * 8 * a.E;
-  const long grid = n_items < (1L << 20) ? n_items : (1L << 20);
-  if (a.row_ids)
-    hipLaunchKernelGGL((grouped_dw_kernel<OUT, true>), dim3(unsigned(grid)), dim3(64 * GT_WAVES), 0, st, a);
-  else
-    hipLaunchKernelGGL((grouped_dw_kernel<OUT, false>), dim3(unsigned(grid)), dim3(64 * GT_WAVES), 0, st, a);
+  const dim3 grid(unsigned(n_items < GT_GRID ? n_items : GT_GRID));
+  if (a.row_ids) {
+    uint64_t* const table = reinterpret_cast<uint64_t*>(ws);
+    const long entries = zero_row_entry(a);
+    const long n = std::max(entries, long(a.K));
+    hipLaunchKernelGGL(row_table_kernel, dim3(unsigned((n + 255) / 256)), dim3(256), 0, st, a, table,
+                       reinterpret_cast<uint16_t*>(table + entries));
+    a.row_table = table;
+    hipLaunchKernelGGL((grouped_dw_kernel<OUT, true>), grid, dim3(64 * GT_WAVES), 0, st, a);
+  } else {
+    hipLaunchKernelGGL((grouped_dw_kernel<OUT, false>), grid, dim3(64 * GT_WAVES), 0, st, a);
+  }
   return hipGetLastError();
 }
 
@@ -575,14 +674,19 @@ bool grouped_tile_fits(const GroupedArgs& a, int which, int in_dt) {
   return in_dt == DT_BF16 && a.K % 8 == 0 && (which == GM_FORWARD || a.N % 8 == 0);
 }
 
-hipError_t launch_grouped_tile(const GroupedArgs& a, int which, int in_dt, int out_dt, hipStream_t st) {
+size_t grouped_tile_workspace(const GroupedArgs& a, int which, int in_dt) {
+  if (which != GM_GRAD_W || !grouped_tile_fits(a, which, in_dt)) return 0;
+  return size_t(zero_row_entry(a)) * 8 + size_t(a.K) * 2;    // the rows' addresses and a row of zeros
+}
+
+hipError_t launch_grouped_tile(const GroupedArgs& a, int which, int in_dt, int out_dt, void* ws, hipStream_t st) {
   if (in_dt == DT_I8)
     return out_dt == DT_F32 ? launch_rows<DT_I8, DT_F32, GM_FORWARD>(a, st) : launch_rows<DT_I8, DT_BF16, GM_FORWARD>(a, st);
   if (which == GM_FORWARD)
     return out_dt == DT_F32 ? launch_rows<DT_BF16, DT_F32, GM_FORWARD>(a, st)
                             : launch_rows<DT_BF16, DT_BF16, GM_FORWARD>(a, st);
   if (which == GM_GRAD_X) return launch_rows<DT_BF16, DT_BF16, GM_GRAD_X>(a, st);
-  return out_dt == DT_F32 ? launch_dw<DT_F32>(a, st) : launch_dw<DT_BF16>(a, st);
+  return out_dt == DT_F32 ? launch_dw<DT_F32>(a, ws, st) : launch_dw<DT_BF16>(a, ws, st);
 }
 
 }  // namespace moe
