@@ -349,37 +349,71 @@ __device__ __forceinline__ void store_tile(uint8_t* mine, const Acc (&acc)[NI][2
     }
 }
 
-// A resident work-group (one per CU: the ring is all of its LDS) takes its
-// items one after another, and while the outputs of one are written the first
-// loads of the next are under way.
-constexpr int GT_GRID = 256;
-
 // ------------------------------------------------------- forward and dx --
 // Item list: (column group, row tile, column) over the row tiles that the
 // segments fill.  Column groups are GT_CG tiles wide, row tiles go in order
 // within a group and columns inside them, so that consecutive items share an
 // expert's weights or a row tile; each XCD (work-group b runs on XCD b % 8)
-// takes one contiguous eighth.
+// takes one contiguous eighth.  Work-groups are dispatched as CUs fall free:
+// tiles of few rows take less time, and a fixed share for resident work-groups
+// was 3 % slower for the 4096-token prompt.
+// The items left over by the last whole round of an XCD's GT_P CUs, m of them,
+// are cut along q into GT_P / m parts (whole stages, at least GT_MIN_PART of
+// them); a second kernel adds the parts' sums in order.  That is also how a
+// call with fewer tiles than CUs fills the chip.
+constexpr int GT_P = 32;
 constexpr int GT_CG = 4;
+constexpr int GT_MIN_PART = 8;
+constexpr int GT_MAXSPLIT = 4;
 
 struct RowsItem {
   int e, row0, rows, n0;       // expert, first sorted row, rows (at most 256; 0: there is no item), first column
-  __device__ __forceinline__ int blocks() const { return rows > 128 ? 4 : (rows > 64 ? 2 : 1); }   // NI
+  int part, parts;             // the part-th of `parts` cuts along q
+  int slot;                    // parts > 1: where its sums go
+};
+
+// An XCD's share of the list.
+struct ListShare {
+  long begin, n, whole;        // first item, items, items that are not cut
+  int left, parts;             // the others, and the parts each is cut into
+  __device__ __forceinline__ ListShare(long n_items, int xcd, int max_parts) {
+    begin = xcd * n_items / 8;
+    n = (xcd + 1) * n_items / 8 - begin;
+    left = int(n % GT_P);
+    parts = left ? min(GT_P / left, max_parts) : 1;
+    if (parts < 2) left = 0, parts = 1;
+    whole = n - left;
+  }
 };
 
 template <int WHICH>
-__device__ __forceinline__ RowsItem rows_item(const GroupedArgs& a, long it) {
-  const int n_ct = ((WHICH == GM_FORWARD ? a.N : a.K) + GT_N - 1) / GT_N, xcd = blockIdx.x & 7;
-  const RowTiles tiles(a, 256);
-  const long n_items = long(tiles.total) * n_ct;
-  const long item = xcd * n_items / 8 + it;
-  if (item >= (xcd + 1) * n_items / 8) return RowsItem{0, 0, 0, 0};
+__device__ __forceinline__ RowsItem list_item(const GroupedArgs& a, const RowTiles& tiles, long item) {
+  const int n_ct = ((WHICH == GM_FORWARD ? a.N : a.K) + GT_N - 1) / GT_N;
   const long per_group = long(tiles.total) * GT_CG;
   const int g = int(item / per_group), in_g = int(item - g * per_group);
   const int width = min(GT_CG, n_ct - g * GT_CG);
   const RowTile rt = tiles.at(in_g / width, 256);
-  return RowsItem{rt.e, rt.begin, min(rt.n, 256), __builtin_amdgcn_readfirstlane((g * GT_CG + in_g % width) * GT_N)};
+  return RowsItem{rt.e, rt.begin, min(rt.n, 256), __builtin_amdgcn_readfirstlane((g * GT_CG + in_g % width) * GT_N), 0, 1, 0};
 }
+
+// The i-th piece of work of this work-group's XCD.
+template <int WHICH>
+__device__ __forceinline__ RowsItem rows_item(const GroupedArgs& a, long i) {
+  const int n_ct = ((WHICH == GM_FORWARD ? a.N : a.K) + GT_N - 1) / GT_N, xcd = blockIdx.x & 7;
+  const RowTiles tiles(a, 256);
+  const ListShare s(long(tiles.total) * n_ct, xcd, a.max_parts);
+  if (i >= s.whole + s.left * s.parts) return RowsItem{0, 0, 0, 0, 0, 1, 0};
+  if (i < s.whole) return list_item<WHICH>(a, tiles, s.begin + i);
+  const int u = int(i - s.whole), part = u / s.left;
+  RowsItem it = list_item<WHICH>(a, tiles, s.begin + s.whole + (u - part * s.left));
+  it.part = __builtin_amdgcn_readfirstlane(part);
+  it.parts = __builtin_amdgcn_readfirstlane(s.parts);
+  it.slot = __builtin_amdgcn_readfirstlane(xcd * GT_P + u);
+  return it;
+}
+
+// Sums of a part: a tile of 256 columns.
+__device__ __forceinline__ float* part_sums(const GroupedArgs& a, int slot) { return a.parts + size_t(slot) * (256 * GT_N); }
 
 // Addresses of one tile.  Rows without a source, and rows past the segment,
 // load some row that exists (w's first, or the tile's first of dy): their
@@ -401,18 +435,24 @@ struct RowsAddr {
     const int lane = threadIdx.x & 63;
     wv = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
     const int n_cols = WHICH == GM_FORWARD ? a.N : a.K;
-    n_q = WHICH == GM_FORWARD ? a.K : a.N;
+    // this part's values of q: whole stages from t0 on, but for the end of the last part
+    constexpr int Q = GT_STAGE / int(sizeof(T));
+    const int all = WHICH == GM_FORWARD ? a.K : a.N, stages = (all + Q - 1) / Q;
+    const int t0 = __builtin_amdgcn_readfirstlane(stages * it.part / it.parts);
+    const int t1 = __builtin_amdgcn_readfirstlane(stages * (it.part + 1) / it.parts);
+    n_q = min(all, t1 * Q) - t0 * Q;
     row_bytes = size_t(n_q) * sizeof(T);
     step_b = BQ ? GT_STAGE : size_t(64) * a.K * sizeof(T);
     const T* const w = reinterpret_cast<const T*>(a.w) + size_t(it.e) * a.N * a.K;
-    w0 = reinterpret_cast<const uint8_t*>(w + (BQ ? size_t(it.n0) * a.K : size_t(it.n0)));
-    dy0 = reinterpret_cast<const uint8_t*>(reinterpret_cast<const T*>(a.dy) + size_t(it.row0) * a.N);
+    w0 = reinterpret_cast<const uint8_t*>(w + (BQ ? size_t(it.n0) * a.K : size_t(it.n0))) + t0 * step_b;
+    dy0 = reinterpret_cast<const uint8_t*>(reinterpret_cast<const T*>(a.dy) + size_t(it.row0) * a.N) + size_t(t0) * GT_STAGE;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = Share<true>::row(wv, i, lane), c = Share<true>::chunk(wv, i, lane) * 16;
       if constexpr (WHICH == GM_FORWARD) {
         const int src = r < it.rows ? source_row(a, it.row0 + r) : -1;
-        pa[i] = reinterpret_cast<const uint8_t*>(src < 0 ? w : reinterpret_cast<const T*>(a.x) + size_t(src) * a.K) + c;
+        pa[i] = reinterpret_cast<const uint8_t*>(src < 0 ? w : reinterpret_cast<const T*>(a.x) + size_t(src) * a.K) +
+                size_t(t0) * GT_STAGE + c;
       } else {
         oa[i] = uint32_t(r < it.rows ? r : 0) * uint32_t(a.N * int(sizeof(T))) + c;
       }
@@ -446,12 +486,16 @@ struct RowsAddr {
   __device__ __forceinline__ void ahead(int) {}
 };
 
-// The products and outputs of tile `cur`; between them the first loads of `next`.
 template <int DT, int OUT, int WHICH, int NI>
-__device__ __forceinline__ void rows_tile(const GroupedArgs& a, uint8_t* smem, RowsAddr<DT, WHICH>& ad,
-                                          const RowsItem& cur, const RowsItem& next, float scale) {
+__device__ __forceinline__ void rows_tile(const GroupedArgs& a, uint8_t* smem, RowsAddr<DT, WHICH>& ad, const RowsItem& it) {
   const int wv = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
   const int n_cols = WHICH == GM_FORWARD ? a.N : a.K;
+  // the row's scale (8-bit), or 1; 0 for a row that stands for zeros
+  float scale = 0.f;
+  if (WHICH == GM_FORWARD && int(threadIdx.x) < it.rows) {
+    const int src = source_row(a, it.row0 + int(threadIdx.x));
+    scale = src < 0 ? 0.f : (DT == DT_I8 ? a.x_scale[src] : 1.f);
+  }
   typename Elem<DT>::acc acc[NI][2];
 #pragma unroll
   for (int i = 0; i < NI; ++i)
@@ -461,18 +505,21 @@ __device__ __forceinline__ void rows_tile(const GroupedArgs& a, uint8_t* smem, R
       for (int q = 0; q < 16; ++q) acc[i][j][q] = 0;
   tile_products<DT, true, WHICH == GM_FORWARD, NI>(smem, ad, acc);
 
-  stage_barrier();                               // every wave is through with the ring
   float* const row_scale = reinterpret_cast<float*>(smem + GT_OUT + GT_WAVES * GT_OUT_WAVE);
+  stage_barrier();                               // every wave is through with the ring
   if (WHICH == GM_FORWARD && threadIdx.x < 256) row_scale[threadIdx.x] = scale;
-  if (next.rows) {
-    ad.set(a, next);
-    first_loads<DT>(smem, ad, next.blocks());
-  }
   stage_barrier();
   const int m0 = (wv >> 2) * 32 * NI;
+  uint8_t* const mine = smem + GT_OUT + wv * GT_OUT_WAVE;
+  if (it.parts > 1) {                            // the sums as they are
+    store_tile<DT_F32, NI>(
+        mine, acc, part_sums(a, it.slot), m0, m0, it.rows, (wv & 3) * 64, GT_N, [](int) { return 0.f; },
+        [](auto x, int, float) { return __builtin_bit_cast(float, x); });
+    return;
+  }
   store_tile<OUT, NI>(
-      smem + GT_OUT + wv * GT_OUT_WAVE, acc, a.out, m0, cur.row0 + m0, cur.row0 + cur.rows, cur.n0 + (wv & 3) * 64, n_cols,
-      [&](int n) { return DT == DT_I8 ? a.w_scale[size_t(cur.e) * a.N + n] : 0.f; },
+      mine, acc, a.out, m0, it.row0 + m0, it.row0 + it.rows, it.n0 + (wv & 3) * 64, n_cols,
+      [&](int n) { return DT == DT_I8 ? a.w_scale[size_t(it.e) * a.N + n] : 0.f; },
       [&](auto x, int r, float ws) {
         if constexpr (DT == DT_I8) return float(x) * row_scale[r] * ws;
         else return WHICH == GM_FORWARD && row_scale[r] == 0.f ? 0.f : float(x);
@@ -482,43 +529,97 @@ __device__ __forceinline__ void rows_tile(const GroupedArgs& a, uint8_t* smem, R
 template <int DT, int OUT, int WHICH>
 __global__ void __launch_bounds__(64 * GT_WAVES) grouped_rows_kernel(GroupedArgs a) {
   __shared__ __attribute__((aligned(16))) uint8_t smem[GT_LDS];
-  long it = blockIdx.x >> 3;
-  RowsItem cur = rows_item<WHICH>(a, it);
-  if (!cur.rows) return;
-  RowsAddr<DT, WHICH> ad;
-  ad.set(a, cur);
-  first_loads<DT>(smem, ad, cur.blocks());
-  while (true) {
-    // the row's scale (8-bit), or 1; 0 for a row that stands for zeros
-    float scale = 0.f;
-    if (WHICH == GM_FORWARD && int(threadIdx.x) < cur.rows) {
-      const int src = source_row(a, cur.row0 + int(threadIdx.x));
-      scale = src < 0 ? 0.f : (DT == DT_I8 ? a.x_scale[src] : 1.f);
-    }
-    it += gridDim.x >> 3;
-    const RowsItem next = rows_item<WHICH>(a, it);
+  for (long i = blockIdx.x >> 3;; i += gridDim.x >> 3) {
+    const RowsItem it = rows_item<WHICH>(a, i);
+    if (!it.rows) return;
+    RowsAddr<DT, WHICH> ad;
+    ad.set(a, it);
     // the last rows of a segment take the smallest tile that holds them
-    if (cur.rows > 128) rows_tile<DT, OUT, WHICH, 4>(a, smem, ad, cur, next, scale);
-    else if (cur.rows > 64) rows_tile<DT, OUT, WHICH, 2>(a, smem, ad, cur, next, scale);
-    else rows_tile<DT, OUT, WHICH, 1>(a, smem, ad, cur, next, scale);
-    if (!next.rows) return;
-    cur = next;
+    first_loads<DT>(smem, ad, it.rows > 128 ? 4 : (it.rows > 64 ? 2 : 1));
+    if (it.rows > 128) rows_tile<DT, OUT, WHICH, 4>(a, smem, ad, it);
+    else if (it.rows > 64) rows_tile<DT, OUT, WHICH, 2>(a, smem, ad, it);
+    else rows_tile<DT, OUT, WHICH, 1>(a, smem, ad, it);
+    stage_barrier();                             // the ring is free for the next item
   }
 }
 
+// Adds the parts of the items that were cut, in order, and writes the outputs:
+// a work-group per 16 rows of an item.
+constexpr int GT_JOIN_ROWS = 16;
 template <int DT, int OUT, int WHICH>
-hipError_t launch_rows(const GroupedArgs& a, hipStream_t st) {
-  const long n_ct = ((WHICH == GM_FORWARD ? a.N : a.K) + GT_N - 1) / GT_N;
-  const long n_items = (long(a.rows) / 256 + (a.E < a.rows ? a.E : a.rows)) * n_ct;   // segments may end in part of a tile
-  const long grid = n_items < GT_GRID ? (n_items + 7) / 8 * 8 : GT_GRID;
+__global__ void __launch_bounds__(256) grouped_join_kernel(GroupedArgs a) {
+  typedef typename std::conditional<DT == DT_I8, i32x4_t, f32x4_t>::type V;
+  const int n_cols = WHICH == GM_FORWARD ? a.N : a.K, n_ct = (n_cols + GT_N - 1) / GT_N;
+  const int chunk = blockIdx.x % (256 / GT_JOIN_ROWS), xcd = blockIdx.x / (256 / GT_JOIN_ROWS), u0 = blockIdx.y;
+  const RowTiles t(a, 256);
+  const ListShare s(long(t.total) * n_ct, xcd, a.max_parts);
+  if (u0 >= s.left) return;
+  const RowsItem it = list_item<WHICH>(a, t, s.begin + s.whole + u0);
+  const int c = (threadIdx.x & 63) * 4, n = it.n0 + c;
+  if (n >= n_cols) return;
+  for (int r = chunk * GT_JOIN_ROWS + int(threadIdx.x >> 6); r < min(it.rows, (chunk + 1) * GT_JOIN_ROWS); r += 4) {
+    V v = {0, 0, 0, 0};
+    for (int p = 0; p < s.parts; ++p)
+      v += *reinterpret_cast<const V*>(part_sums(a, xcd * GT_P + p * s.left + u0) + r * GT_N + c);
+    float o[4];
+    const int src = WHICH == GM_FORWARD ? source_row(a, it.row0 + r) : 0;
+    const float xs = DT == DT_I8 && src >= 0 ? a.x_scale[src] : 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (DT == DT_I8) o[i] = n + i < n_cols ? float(v[i]) * xs * a.w_scale[size_t(it.e) * a.N + n + i] : 0.f;
+      else o[i] = src < 0 ? 0.f : float(v[i]);
+    }
+    const size_t at = size_t(it.row0 + r) * n_cols + n;
+    if (n_cols % 4 == 0) {
+      if constexpr (OUT == DT_F32)
+        *reinterpret_cast<f32x4_t*>(reinterpret_cast<float*>(a.out) + at) = f32x4_t{o[0], o[1], o[2], o[3]};
+      else
+        *reinterpret_cast<u32x2_t*>(reinterpret_cast<uint16_t*>(a.out) + at) =
+            u32x2_t{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3])};
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (n + i < n_cols) store_out<OUT>(a.out, at + i, o[i]);
+    }
+  }
+}
+
+// The most items a call can have (the host does not know the segments), and
+// the most parts that an item of its shape is cut into (1: nothing is cut).
+struct RowsPlan {
+  long items;
+  int max_parts;
+};
+RowsPlan rows_plan(const GroupedArgs& a, int which, int in_dt) {
+  const long n_cols = which == GM_FORWARD ? a.N : a.K, n_q = which == GM_FORWARD ? a.K : a.N;
+  const long stages = (n_q * (in_dt == DT_I8 ? 1 : 2) + GT_STAGE - 1) / GT_STAGE;
+  RowsPlan p{(long(a.rows) / 256 + std::min(a.E, a.rows)) * ((n_cols + GT_N - 1) / GT_N), 1};
+  // With many rounds the CUs that idle in the last one matter little, and the second launch is saved.
+  if (p.items <= GT_MAXSPLIT * 8 * GT_P) p.max_parts = int(std::max<long>(1, std::min<long>(stages / GT_MIN_PART, GT_P)));
+  return p;
+}
+
+template <int DT, int OUT, int WHICH>
+hipError_t launch_rows(const GroupedArgs& args, void* ws, hipStream_t st) {
+  GroupedArgs a = args;
+  const RowsPlan p = rows_plan(a, WHICH, DT);
+  a.parts = reinterpret_cast<float*>(ws);
+  a.max_parts = p.max_parts;
+  const long grid = std::min<long>((p.items + 7) / 8 * 8 + (p.max_parts > 1 ? 8 * GT_P : 0), 1L << 20);
   hipLaunchKernelGGL((grouped_rows_kernel<DT, OUT, WHICH>), dim3(unsigned(grid)), dim3(64 * GT_WAVES), 0, st, a);
+  if (p.max_parts > 1)
+    hipLaunchKernelGGL((grouped_join_kernel<DT, OUT, WHICH>), dim3(8 * (256 / GT_JOIN_ROWS), GT_P / 2), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 
 // -------------------------------------------------------------------- dw --
-// One item per 256 x 256 tile of dw[e]; the reduction runs over e's rows.
+// One item per 256 x 256 tile of dw[e]; the reduction runs over e's rows.  A
+// resident work-group (one per CU: the ring is all of its LDS) takes its items
+// one after another, and while the outputs of one are written the first loads
+// of the next are under way.
 // Experts' work differs with their rows, so each XCD takes an eighth of every
 // expert's tiles, in order (they share panels of dy and x in that XCD's L2).
+constexpr int GT_GRID = 256;
 struct DwItem {
   int e, m0, n0, begin, n;     // expert (-1: there is no item), tile of dw[e], e's segment
 };
@@ -675,17 +776,20 @@ bool grouped_tile_fits(const GroupedArgs& a, int which, int in_dt) {
 }
 
 size_t grouped_tile_workspace(const GroupedArgs& a, int which, int in_dt) {
-  if (which != GM_GRAD_W || !grouped_tile_fits(a, which, in_dt)) return 0;
+  if (!grouped_tile_fits(a, which, in_dt)) return 0;
+  if (which != GM_GRAD_W)      // the parts' sums, a tile for each CU
+    return rows_plan(a, which, in_dt).max_parts > 1 ? size_t(8 * GT_P) * 256 * GT_N * 4 : 0;
   return size_t(zero_row_entry(a)) * 8 + size_t(a.K) * 2;    // the rows' addresses and a row of zeros
 }
 
 hipError_t launch_grouped_tile(const GroupedArgs& a, int which, int in_dt, int out_dt, void* ws, hipStream_t st) {
   if (in_dt == DT_I8)
-    return out_dt == DT_F32 ? launch_rows<DT_I8, DT_F32, GM_FORWARD>(a, st) : launch_rows<DT_I8, DT_BF16, GM_FORWARD>(a, st);
+    return out_dt == DT_F32 ? launch_rows<DT_I8, DT_F32, GM_FORWARD>(a, ws, st)
+                             : launch_rows<DT_I8, DT_BF16, GM_FORWARD>(a, ws, st);
   if (which == GM_FORWARD)
-    return out_dt == DT_F32 ? launch_rows<DT_BF16, DT_F32, GM_FORWARD>(a, st)
-                            : launch_rows<DT_BF16, DT_BF16, GM_FORWARD>(a, st);
-  if (which == GM_GRAD_X) return launch_rows<DT_BF16, DT_BF16, GM_GRAD_X>(a, st);
+    return out_dt == DT_F32 ? launch_rows<DT_BF16, DT_F32, GM_FORWARD>(a, ws, st)
+                            : launch_rows<DT_BF16, DT_BF16, GM_FORWARD>(a, ws, st);
+  if (which == GM_GRAD_X) return launch_rows<DT_BF16, DT_BF16, GM_GRAD_X>(a, ws, st);
   return out_dt == DT_F32 ? launch_dw<DT_F32>(a, ws, st) : launch_dw<DT_BF16>(a, ws, st);
 }
 
