@@ -38,6 +38,13 @@ __device__ __forceinline__ void mma16(u32x4_t a, u32x4_t b, Acc& c) {
   }
 }
 
+// Two floats to bf16, to nearest even, by the hardware's conversion.
+__device__ __forceinline__ uint32_t cvt_pk_bf16(float lo, float hi) {
+  typedef float f32x2_t __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{lo, hi}, bf16x2_t));
+}
+
 template <int OUT>
 __device__ __forceinline__ void store_out(void* out, size_t i, float v) {
   if constexpr (OUT == DT_F32) reinterpret_cast<float*>(out)[i] = v;

@@ -135,7 +135,7 @@ __device__ __forceinline__ void stream_tiles(const GroupedArgs& a, float* smem, 
       if constexpr (OUT == DT_F32) *reinterpret_cast<f32x4_t*>(reinterpret_cast<float*>(a.out) + at) = f32x4_t{o[0], o[1], o[2], o[3]};
       else
         *reinterpret_cast<u32x2_t*>(reinterpret_cast<uint16_t*>(a.out) + at) =
-            u32x2_t{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3])};
+            u32x2_t{cvt_pk_bf16(o[0], o[1]), cvt_pk_bf16(o[2], o[3])};
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i)

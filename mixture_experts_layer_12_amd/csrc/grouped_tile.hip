@@ -216,7 +216,7 @@ __device__ __forceinline__ void tile_products(uint8_t* smem, Addr& ad, typename 
 #pragma unroll
     for (int i = 0; i < NI; ++i)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) mma16<DT>(f.a[h][i], f.b[h][j], acc[i][j]);
+      for (int j = 0; j < 2; ++j) mma16<DT>(f.b[h][j], f.a[h][i], acc[i][j]);
   };
   // One k-step in a fixed order: the MFMAs of parity h, between them the reads of k-step ks of the slots
   // at_a / at_b, and after those, one to an MFMA, the loads 0 .. V - 1 that `load` issues.
@@ -225,7 +225,7 @@ __device__ __forceinline__ void tile_products(uint8_t* smem, Addr& ad, typename 
     constexpr int PER = (R + M - 1) / M > 1 ? (R + M - 1) / M : (R > M - V ? 2 : 1);   // reads after an MFMA
     for_range<0, M>([&](auto qc) {
       constexpr int q = decltype(qc)::value;
-      mma16<DT>(f.a[h][q / 2], f.b[h][q % 2], acc[q / 2][q % 2]);
+      mma16<DT>(f.b[h][q % 2], f.a[h][q / 2], acc[q / 2][q % 2]);
       for_range<(q * PER < R ? q * PER : R), ((q + 1) * PER < R ? (q + 1) * PER : R)>(
           [&](auto r) { read_one(at_a, at_b, ks, r); });
       if constexpr (q >= M - V) load(std::integral_constant<int, q - (M - V)>{});
@@ -281,72 +281,69 @@ __device__ __forceinline__ void tile_products(uint8_t* smem, Addr& ad, typename 
 }
 
 // Writes a wave's 32 NI x 64 part of a tile: rows from `row` (those below
-// `end`), columns from `col` (below n_cols) of the row-major `out`.  `value(x,
-// r, s)` makes the output of sum x in row r of the tile, s = `col_scale(n)`.
-// The sums go through LDS, 16 rows of bf16 or 8 of fp32 at a time, so that a
-// store instruction covers whole 128-byte lines (stored as they lie in
-// registers, in 64-byte pieces of bf16, the outputs of a tile took longer than
-// 4 stages of the main loop).  Rows of out that are not 16-byte aligned are
-// stored element by element.  `mine`: the wave's GT_OUT_WAVE bytes.
-constexpr int GT_OUT_WAVE = 16 * (64 * 2 + 16);   // rows padded by 16 bytes for the banks
-static_assert(8 * (64 * 4 + 16) <= GT_OUT_WAVE, "8 rows of fp32");
-constexpr int GT_OUT = 4 * GT_SLOT;               // the waves' areas start at slot 4; then 256 row scales
-static_assert(GT_WAVES * GT_OUT_WAVE + 256 * 4 <= GT_SLOT, "one slot");
-template <int OUT, int NI, class Acc, class Value, class Scale>
-__device__ __forceinline__ void store_tile(uint8_t* mine, const Acc (&acc)[NI][2], void* out, int tile_row, int row,
-                                           int end, int col, int n_cols, Scale col_scale, Value value) {
-  constexpr int B = OUT == DT_F32 ? 4 : 2, C = 16 / B;
-  constexpr int LPR = 64 / C, RPI = 64 / LPR;     // lanes per row and rows per store instruction
-  constexpr int CR = OUT == DT_F32 ? 8 : 16, ROW = 64 * B + 16;   // rows staged at a time, bytes of one
+// `end`), columns from `col` (below n_cols) of the row-major `out`.
+// `value(acc, q, i, j, n, v)` makes the outputs v[0 .. 3] of columns n .. n + 3
+// from the sums q .. q + 3 of block (i, j).  The MFMAs take B as their first
+// operand, so that a lane holds four neighbouring columns of one row; 32 rows
+// by 128 bytes at a time they go through LDS, so that a store instruction
+// covers whole 128-byte lines.  16-byte units are permuted within the rows
+// there (the lanes of one access lie 128 bytes apart).  Rows of out that are
+// not 16-byte aligned are stored element by element.
+constexpr int GT_OUT_WAVE = 32 * 128;             // bytes per wave, from slot 4 on
+constexpr int GT_OUT = 4 * GT_SLOT;
+static_assert(GT_WAVES * GT_OUT_WAVE <= GT_SLOT, "one slot");
+template <int OUT, int NI, class Acc, class Value>
+__device__ __forceinline__ void store_tile(uint8_t* smem, const Acc (&acc)[NI][2], void* out, int row, int end, int col,
+                                           int n_cols, Value value) {
+  constexpr int B = OUT == DT_F32 ? 4 : 2, C = 16 / B, HALVES = OUT == DT_F32 ? 2 : 1;
+  uint8_t* const mine = smem + GT_OUT + __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6)) * GT_OUT_WAVE;
   const int lane = lane_here(), l32 = lane & 31, hi = lane >> 5;
-  // register q of lane l: row 8 (q / 4) + 4 (l / 32) + q % 4 of a 32 x 32 block, column l % 32
-  float s[2];
+  uint8_t* const base = reinterpret_cast<uint8_t*>(out);
+  // register q of lane l: column 8 (q / 4) + 4 (l / 32) + q % 4 of a 32 x 32 block, row l % 32
 #pragma unroll
-  for (int j = 0; j < 2; ++j) s[j] = col + 32 * j + l32 < n_cols ? col_scale(col + 32 * j + l32) : 0.f;
-  if (n_cols % C) {
+  for (int i = 0; i < NI; ++i) {
+    const int first = row + 32 * i;
+    if (first >= end) return;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int n = col + 32 * j + l32;
-      if (n >= n_cols) continue;
+    for (int half = 0; half < HALVES; ++half) {
 #pragma unroll
-      for (int i = 0; i < NI; ++i)
+      for (int jj = 0; jj < 2 / HALVES; ++jj)
 #pragma unroll
-        for (int q = 0; q < 16; ++q) {
-          const int r = 32 * i + 8 * (q >> 2) + 4 * hi + (q & 3);
-          if (row + r < end) store_out<OUT>(out, size_t(row + r) * n_cols + n, value(acc[i][j][q], tile_row + r, s[j]));
-        }
-    }
-    return;
-  }
-  const int cr = lane / LPR, cc = (lane % LPR) * C;
-#pragma unroll
-  for (int i = 0; i < NI; ++i)
-#pragma unroll
-    for (int h = 0; h < 32 / CR; ++h) {
-      const int first = 32 * i + CR * h;
-      if (row + first >= end) return;
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int q = h * CR / 2; q < (h + 1) * CR / 2; ++q) {
-          const int r = 8 * (q >> 2) + 4 * hi + (q & 3);
-          const float v = value(acc[i][j][q], tile_row + 32 * i + r, s[j]);
-          uint8_t* p = mine + (r - CR * h) * ROW + (32 * j + l32) * B;
-          if constexpr (OUT == DT_F32) *reinterpret_cast<float*>(p) = v;
-          else *reinterpret_cast<uint16_t*>(p) = uint16_t(f32_to_bf16(v));
+        for (int g = 0; g < 4; ++g) {
+          const int j = half + jj;
+          float v[4];
+          value(acc[i][j], 4 * g, i, j, col + 32 * j + 8 * g + 4 * hi, v);
+          if constexpr (OUT == DT_F32)
+            *reinterpret_cast<f32x4_t*>(mine + l32 * 128 + (((2 * g + hi) ^ (l32 & 7)) << 4)) = f32x4_t{v[0], v[1], v[2], v[3]};
+          else
+            *reinterpret_cast<u32x2_t*>(mine + l32 * 128 + (((4 * j + g) ^ (l32 & 7)) << 4) + 8 * hi) =
+                u32x2_t{cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3])};
         }
       // LDS serves a wave's accesses in order; the compiler has to keep it
       asm volatile("" ::: "memory");
+      const int c0 = col + 32 * half;              // the columns that are staged begin here
+      if (n_cols % C == 0) {
 #pragma unroll
-      for (int k = 0; k < CR / RPI; ++k) {
-        const int r = k * RPI + cr;
-        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(mine + r * ROW + cc * B);
-        if (row + first + r < end && col + cc < n_cols)
-          *reinterpret_cast<u32x4_t*>(reinterpret_cast<uint8_t*>(out) +
-                                      (size_t(row + first + r) * n_cols + col + cc) * B) = v;
+        for (int k = 0; k < 4; ++k) {
+          const int r = k * 8 + (lane >> 3), c = c0 + (lane & 7) * C;
+          const u32x4_t v = *reinterpret_cast<const u32x4_t*>(mine + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+          if (first + r < end && c < n_cols)
+            *reinterpret_cast<u32x4_t*>(base + (size_t(first + r) * n_cols + c) * B) = v;
+        }
+      } else {
+        constexpr int LPR = 128 / B;               // a lane per element: 64 of bf16, 32 of fp32 in a row
+        const int c = lane % LPR;
+        if (c0 + c < n_cols)
+          for (int r = lane / LPR; r < 32 && first + r < end; r += 64 / LPR) {
+            const uint8_t* p = mine + r * 128 + (((c / C) ^ (r & 7)) << 4) + (c % C) * B;
+            uint8_t* const q = base + (size_t(first + r) * n_cols + c0 + c) * B;
+            if constexpr (OUT == DT_F32) *reinterpret_cast<float*>(q) = *reinterpret_cast<const float*>(p);
+            else *reinterpret_cast<uint16_t*>(q) = *reinterpret_cast<const uint16_t*>(p);
+          }
       }
       asm volatile("" ::: "memory");
     }
+  }
 }
 
 // ------------------------------------------------------- forward and dx --
@@ -505,25 +502,44 @@ __device__ __forceinline__ void rows_tile(const GroupedArgs& a, uint8_t* smem, R
       for (int q = 0; q < 16; ++q) acc[i][j][q] = 0;
   tile_products<DT, true, WHICH == GM_FORWARD, NI>(smem, ad, acc);
 
-  float* const row_scale = reinterpret_cast<float*>(smem + GT_OUT + GT_WAVES * GT_OUT_WAVE);
+  float* const row_scale = reinterpret_cast<float*>(smem);
   stage_barrier();                               // every wave is through with the ring
   if (WHICH == GM_FORWARD && threadIdx.x < 256) row_scale[threadIdx.x] = scale;
   stage_barrier();
-  const int m0 = (wv >> 2) * 32 * NI;
-  uint8_t* const mine = smem + GT_OUT + wv * GT_OUT_WAVE;
+  const int m0 = (wv >> 2) * 32 * NI, c0 = it.n0 + (wv & 3) * 64;
   if (it.parts > 1) {                            // the sums as they are
-    store_tile<DT_F32, NI>(
-        mine, acc, part_sums(a, it.slot), m0, m0, it.rows, (wv & 3) * 64, GT_N, [](int) { return 0.f; },
-        [](auto x, int, float) { return __builtin_bit_cast(float, x); });
+    store_tile<DT_F32, NI>(smem, acc, part_sums(a, it.slot), m0, it.rows, (wv & 3) * 64, GT_N,
+                           [](const auto& x, int q, int, int, int, float(&v)[4]) {
+#pragma unroll
+                             for (int t = 0; t < 4; ++t) {
+                               const auto sum = x[q + t];
+                               v[t] = __builtin_bit_cast(float, sum);
+                             }
+                           });
     return;
   }
-  store_tile<OUT, NI>(
-      mine, acc, a.out, m0, it.row0 + m0, it.row0 + it.rows, it.n0 + (wv & 3) * 64, n_cols,
-      [&](int n) { return DT == DT_I8 ? a.w_scale[size_t(it.e) * a.N + n] : 0.f; },
-      [&](auto x, int r, float ws) {
-        if constexpr (DT == DT_I8) return float(x) * row_scale[r] * ws;
-        else return WHICH == GM_FORWARD && row_scale[r] == 0.f ? 0.f : float(x);
-      });
+  const int last = lane_here();
+  float rs[NI], ws[2][16];                       // scales of the lane's rows and columns
+  if constexpr (WHICH == GM_FORWARD)
+#pragma unroll
+    for (int i = 0; i < NI; ++i) rs[i] = row_scale[m0 + 32 * i + (last & 31)];
+  if constexpr (DT == DT_I8)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) {
+        const int n = c0 + 32 * j + 8 * (q >> 2) + 4 * (last >> 5) + (q & 3);
+        ws[j][q] = n < n_cols ? a.w_scale[size_t(it.e) * a.N + n] : 0.f;
+      }
+  store_tile<OUT, NI>(smem, acc, a.out, it.row0 + m0, it.row0 + it.rows, c0, n_cols,
+                      [&](const auto& x, int q, int i, int j, int, float(&v)[4]) {
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) {
+                          if constexpr (DT == DT_I8) v[t] = float(x[q + t]) * rs[i] * ws[j][q + t];
+                          else if constexpr (WHICH == GM_FORWARD) v[t] = rs[i] == 0.f ? 0.f : x[q + t];
+                          else v[t] = x[q + t];
+                        }
+                      });
 }
 
 template <int DT, int OUT, int WHICH>
@@ -575,7 +591,7 @@ __global__ void __launch_bounds__(256) grouped_join_kernel(GroupedArgs a) {
         *reinterpret_cast<f32x4_t*>(reinterpret_cast<float*>(a.out) + at) = f32x4_t{o[0], o[1], o[2], o[3]};
       else
         *reinterpret_cast<u32x2_t*>(reinterpret_cast<uint16_t*>(a.out) + at) =
-            u32x2_t{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3])};
+            u32x2_t{cvt_pk_bf16(o[0], o[1]), cvt_pk_bf16(o[2], o[3])};
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -739,10 +755,11 @@ __global__ void __launch_bounds__(64 * GT_WAVES) grouped_dw_kernel(GroupedArgs a
       first_loads<DT_BF16>(smem, ad, 4);
     }
     const int m = cur.m0 + (wv >> 2) * 128;
-    store_tile<OUT, 4>(
-        smem + GT_OUT + wv * GT_OUT_WAVE, acc,
-        reinterpret_cast<uint8_t*>(a.out) + size_t(cur.e) * a.N * a.K * (OUT == DT_F32 ? 4 : 2), 0, m, a.N,
-        cur.n0 + (wv & 3) * 64, a.K, [](int) { return 0.f; }, [](float x, int, float) { return x; });
+    store_tile<OUT, 4>(smem, acc, reinterpret_cast<uint8_t*>(a.out) + size_t(cur.e) * a.N * a.K * (OUT == DT_F32 ? 4 : 2), m,
+                       a.N, cur.n0 + (wv & 3) * 64, a.K, [](const auto& x, int q, int, int, int, float(&v)[4]) {
+#pragma unroll
+                         for (int t = 0; t < 4; ++t) v[t] = x[q + t];
+                       });
     if (next.e < 0) return;
     cur = next;
   }

@@ -54,8 +54,8 @@ __device__ __forceinline__ void store8(void* base, size_t i, int n, const float 
     uint16_t* p = reinterpret_cast<uint16_t*>(base) + i;
     struct __attribute__((packed, aligned(2))) U { u32x4_t v; };
     if (n >= 8) {
-      reinterpret_cast<U*>(p)->v = u32x4_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
-                                           pack_bf16(v[6], v[7])};
+      reinterpret_cast<U*>(p)->v = u32x4_t{cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3]), cvt_pk_bf16(v[4], v[5]),
+                                           cvt_pk_bf16(v[6], v[7])};
       return;
     }
 #pragma unroll
