@@ -440,128 +440,150 @@ def alloc_grouped_workspace(shape: moe_grouped_shape_t, device="cuda"):
     return torch.empty(max(moe_grouped_workspace_size(shape), 256), dtype=torch.uint8, device=device)
 
 
-_TORCH_NAMES = {MOE_F32: "torch.float32", MOE_BF16: "torch.bfloat16", MOE_I8: "torch.int8", "i32": "torch.int32"}
+_types = None      # torch dtypes of the element codes
 
 
-def _operands(where: str, *specs):
-    """Checks the tensors among ``specs`` ((name, value, dtype code, elements) each): dense, on one GPU, of the
-    type and size that the shape says.  Raw addresses and None pass.  Returns that GPU's index, or None."""
-    device = None
-    for name, t, dtype, n in specs:
-        if t is None or isinstance(t, int):
-            continue
-        if not t.is_contiguous():
-            raise ValueError(f"{where}: {name} is not contiguous")
-        if str(t.dtype) != _TORCH_NAMES[dtype]:
-            raise ValueError(f"{where}: {name} has type {t.dtype}, the shape says {_TORCH_NAMES[dtype]}")
-        if t.numel() < n:
-            raise ValueError(f"{where}: {name} has {t.numel()} elements, the shape needs {n}")
-        index = t.get_device()
-        if index < 0:
-            raise ValueError(f"{where}: {name} is not on a GPU")
-        if device is None:
-            device = index
-        elif index != device:
-            raise ValueError(f"{where}: {name} is on another GPU than the operands before it")
-    return device
+def _torch_types():
+    """The torch dtype of each element code (None for those that no tensor has), looked up once."""
+    global _types
+    if _types is None:
+        import torch
+        _types = {MOE_F32: torch.float32, MOE_BF16: torch.bfloat16, MOE_I8: torch.int8, "i32": torch.int32}
+    return _types
 
 
-def _on_device(device, stream, call):
-    """call(stream handle) with ``device`` (an index, or None) current; stream None is that device's current one."""
+def _device_of(*tensors) -> int:
+    """Index of the GPU that the first tensor lies on (-1: on none); None if all are addresses."""
+    for t in tensors:
+        if t is not None and type(t) is not int:
+            return t.get_device()
+    return None
+
+
+def _checked(where: str, name: str, t, dtype, n: int, device):
+    """The address of operand ``t``: dense, of the type and at least the size that the shape says, on GPU ``device``.
+    Raw addresses and None pass as they are."""
+    if t is None or type(t) is int:
+        return t
+    on = t.get_device()
+    if t.dtype is not dtype or t.numel() < n or on < 0 or (on != device and device is not None) or not t.is_contiguous():
+        if t.dtype is not dtype:
+            why = f"has type {t.dtype}, the shape says {dtype}"
+        elif not t.is_contiguous():
+            why = "is not contiguous"
+        elif t.numel() < n:
+            why = f"has {t.numel()} elements, the shape needs {n}"
+        elif on < 0:
+            why = "is not on a GPU"
+        else:
+            why = "is on another GPU than the operands before it"
+        raise ValueError(f"{where}: {name} {why}")
+    return t.data_ptr()
+
+
+def _launch(where: str, function, device, stream, check: bool, *args) -> int:
+    """function(*args, stream) with GPU ``device`` current; ``stream`` None is that GPU's current stream."""
     import torch
     if device is None or device == torch.cuda.current_device():
-        return call(_stream(stream))
-    with torch.cuda.device(device):
-        return call(_stream(stream))
+        if stream is None and device is not None:
+            st = torch._C._cuda_getCurrentRawStream(device)
+        else:
+            st = _stream(stream)
+        rc = function(*args, st)
+    else:
+        with torch.cuda.device(device):
+            rc = function(*args, _stream(stream))
+    if check and rc:
+        raise MoeError(rc, where)
+    return rc
 
 
-def _grouped_specs(shape, x_name, x, row_ids, offsets, counts):
-    return ((x_name, x, shape.x_dtype, shape.x_rows * shape.K), ("row_ids", row_ids, "i32", shape.rows),
-            ("offsets", offsets, "i32", shape.E + (counts is None)), ("counts", counts, "i32", shape.E))
+def _grouped(where, function, shape, x_name, x, x_scale, dy, row_ids, offsets, counts, w, w_scale, outs, workspace,
+             ws_bytes, stream, check):
+    """The three grouped products: checks the operands and calls ``function`` with those that it takes."""
+    types = _torch_types()
+    rows, N, K, E, x_rows = shape.rows, shape.N, shape.K, shape.E, shape.x_rows
+    dt, i32 = types.get(shape.x_dtype), types["i32"]
+    dev = _device_of(x, dy, w, offsets)
+    px = _checked(where, x_name, x, dt, x_rows * K, dev)
+    ids = _checked(where, "row_ids", row_ids, i32, rows, dev)
+    off = _checked(where, "offsets", offsets, i32, E + (counts is None), dev)
+    cnt = _checked(where, "counts", counts, i32, E, dev)
+    pw = _checked(where, "w", w, dt, E * N * K, dev)
+    po = [_checked(where, name, t, types.get(code), n, dev) for name, t, code, n in outs]
+    if x_name == "xq":
+        f32 = types[MOE_F32]
+        args = (px, _checked(where, "x_scale", x_scale, f32, x_rows, dev), ids, off, cnt, pw,
+                _checked(where, "w_scale", w_scale, f32, E * N, dev))
+    elif len(po) == 2:
+        args = (_checked(where, "dy", dy, dt, rows * N, dev), px, ids, off, cnt, pw)
+    else:
+        args = (px, ids, off, cnt, pw)
+    nb = _nbytes(workspace) if ws_bytes is None else ws_bytes
+    return _launch(where, function, dev, stream, check, ctypes.byref(shape), *args, *po, _ptr(workspace), nb)
 
 
 def moe_grouped_matmul(shape: moe_grouped_shape_t, x, row_ids, offsets, counts, w, y, workspace, ws_bytes=None,
                        stream=None, check=True) -> int:
     """y[r] = x[row(r)] . w[e]^T over the segments; ``row_ids`` and ``counts`` may be None."""
-    dev = _operands("moe_grouped_matmul", *_grouped_specs(shape, "x", x, row_ids, offsets, counts),
-                    ("w", w, shape.x_dtype, shape.E * shape.N * shape.K), ("y", y, shape.out_dtype, shape.rows * shape.N))
-    nb = _nbytes(workspace) if ws_bytes is None else ws_bytes
-    rc = _on_device(dev, stream, lambda st: load_library().moe_grouped_matmul(
-        ctypes.byref(shape), _ptr(x), _ptr(row_ids), _ptr(offsets), _ptr(counts), _ptr(w), _ptr(y), _ptr(workspace),
-        nb, st))
-    if check and rc:
-        raise MoeError(rc, "moe_grouped_matmul")
-    return rc
+    return _grouped("moe_grouped_matmul", load_library().moe_grouped_matmul, shape, "x", x, None, None, row_ids, offsets,
+                    counts, w, None, (("y", y, shape.out_dtype, shape.rows * shape.N),), workspace, ws_bytes, stream,
+                    check)
 
 
 def moe_grouped_matmul_backward(shape: moe_grouped_shape_t, dy, x, row_ids, offsets, counts, w, dx, dw, workspace,
                                 ws_bytes=None, stream=None, check=True) -> int:
     """The gradients dx (sorted order) and dw of moe_grouped_matmul; either may be None."""
-    size = shape.E * shape.N * shape.K
-    dev = _operands("moe_grouped_matmul_backward", *_grouped_specs(shape, "x", x, row_ids, offsets, counts),
-                    ("dy", dy, shape.x_dtype, shape.rows * shape.N), ("w", w, shape.x_dtype, size),
-                    ("dx", dx, shape.x_dtype, shape.rows * shape.K), ("dw", dw, shape.out_dtype, size))
-    nb = _nbytes(workspace) if ws_bytes is None else ws_bytes
-    rc = _on_device(dev, stream, lambda st: load_library().moe_grouped_matmul_backward(
-        ctypes.byref(shape), _ptr(dy), _ptr(x), _ptr(row_ids), _ptr(offsets), _ptr(counts), _ptr(w), _ptr(dx),
-        _ptr(dw), _ptr(workspace), nb, st))
-    if check and rc:
-        raise MoeError(rc, "moe_grouped_matmul_backward")
-    return rc
-
-
-def moe_quantize_rows(x, q, scale, stream=None, check=True) -> int:
-    """8-bit codes ``q`` and fp32 ``scale`` of each row of the matrix ``x`` (float32 or bfloat16, two dimensions)."""
-    if x.dim() != 2 or str(x.dtype) not in ("torch.float32", "torch.bfloat16"):
-        raise ValueError("moe_quantize_rows: x is not a float32 or bfloat16 matrix")
-    dt = MOE_F32 if str(x.dtype) == "torch.float32" else MOE_BF16
-    rows, cols = x.shape
-    dev = _operands("moe_quantize_rows", ("x", x, dt, rows * cols), ("q", q, MOE_I8, rows * cols),
-                    ("scale", scale, MOE_F32, rows))
-    rc = _on_device(dev, stream, lambda st: load_library().moe_quantize_rows(rows, cols, dt, _ptr(x), _ptr(q),
-                                                                             _ptr(scale), st))
-    if check and rc:
-        raise MoeError(rc, "moe_quantize_rows")
-    return rc
+    return _grouped("moe_grouped_matmul_backward", load_library().moe_grouped_matmul_backward, shape, "x", x, None, dy,
+                    row_ids, offsets, counts, w, None,
+                    (("dx", dx, shape.x_dtype, shape.rows * shape.K),
+                     ("dw", dw, shape.out_dtype, shape.E * shape.N * shape.K)), workspace, ws_bytes, stream, check)
 
 
 def moe_grouped_matmul_i8(shape: moe_grouped_shape_t, xq, x_scale, row_ids, offsets, counts, wq, w_scale, y, workspace,
                           ws_bytes=None, stream=None, check=True) -> int:
     """The forward product on 8-bit codes with scales for each row of ``xq`` and each output channel of ``wq``."""
-    dev = _operands("moe_grouped_matmul_i8", *_grouped_specs(shape, "xq", xq, row_ids, offsets, counts),
-                    ("x_scale", x_scale, MOE_F32, shape.x_rows), ("wq", wq, MOE_I8, shape.E * shape.N * shape.K),
-                    ("w_scale", w_scale, MOE_F32, shape.E * shape.N), ("y", y, shape.out_dtype, shape.rows * shape.N))
-    nb = _nbytes(workspace) if ws_bytes is None else ws_bytes
-    rc = _on_device(dev, stream, lambda st: load_library().moe_grouped_matmul_i8(
-        ctypes.byref(shape), _ptr(xq), _ptr(x_scale), _ptr(row_ids), _ptr(offsets), _ptr(counts), _ptr(wq),
-        _ptr(w_scale), _ptr(y), _ptr(workspace), nb, st))
-    if check and rc:
-        raise MoeError(rc, "moe_grouped_matmul_i8")
-    return rc
+    return _grouped("moe_grouped_matmul_i8", load_library().moe_grouped_matmul_i8, shape, "xq", xq, x_scale, None, row_ids,
+                    offsets, counts, wq, w_scale, (("y", y, shape.out_dtype, shape.rows * shape.N),), workspace, ws_bytes,
+                    stream, check)
+
+
+def moe_quantize_rows(x, q, scale, stream=None, check=True) -> int:
+    """8-bit codes ``q`` and fp32 ``scale`` of each row of the matrix ``x`` (float32 or bfloat16, two dimensions)."""
+    types = _torch_types()
+    dt = MOE_F32 if x.dtype is types[MOE_F32] else MOE_BF16
+    if x.dim() != 2 or x.dtype is not types[dt]:
+        raise ValueError("moe_quantize_rows: x is not a float32 or bfloat16 matrix")
+    rows, cols = x.shape
+    dev, where = x.get_device(), "moe_quantize_rows"
+    return _launch(where, load_library().moe_quantize_rows, dev, stream, check, rows, cols, dt,
+                   _checked(where, "x", x, types[dt], rows * cols, dev),
+                   _checked(where, "q", q, types[MOE_I8], rows * cols, dev),
+                   _checked(where, "scale", scale, types[MOE_F32], rows, dev))
 
 
 def moe_combine(shape: moe_combine_shape_t, y, inv, weights, out, stream=None, check=True) -> int:
     """out[t] = sum_j weights[t, j] * y[inv[t, j]]; ``weights`` None means 1."""
-    n = shape.T * shape.top_k
-    dev = _operands("moe_combine", ("y", y, shape.y_dtype, shape.rows * shape.H), ("inv", inv, "i32", n),
-                    ("weights", weights, MOE_F32, n), ("out", out, shape.out_dtype, shape.T * shape.H))
-    rc = _on_device(dev, stream, lambda st: load_library().moe_combine(
-        ctypes.byref(shape), _ptr(y), _ptr(inv), _ptr(weights), _ptr(out), st))
-    if check and rc:
-        raise MoeError(rc, "moe_combine")
-    return rc
+    types, where = _torch_types(), "moe_combine"
+    T, H = shape.T, shape.H
+    n, dev = T * shape.top_k, _device_of(y, inv, out)
+    return _launch(where, load_library().moe_combine, dev, stream, check, ctypes.byref(shape),
+                   _checked(where, "y", y, types.get(shape.y_dtype), shape.rows * H, dev),
+                   _checked(where, "inv", inv, types["i32"], n, dev),
+                   _checked(where, "weights", weights, types[MOE_F32], n, dev),
+                   _checked(where, "out", out, types.get(shape.out_dtype), T * H, dev))
 
 
 def moe_combine_backward(shape: moe_combine_shape_t, dout, y, inv, weights, dy, dweights, stream=None,
                          check=True) -> int:
     """The gradients dy and dweights of moe_combine; either may be None (``y`` is read for dweights only)."""
-    n = shape.T * shape.top_k
-    dev = _operands("moe_combine_backward", ("dout", dout, shape.out_dtype, shape.T * shape.H),
-                    ("y", y, shape.y_dtype, shape.rows * shape.H), ("inv", inv, "i32", n),
-                    ("weights", weights, MOE_F32, n), ("dy", dy, shape.y_dtype, shape.rows * shape.H),
-                    ("dweights", dweights, MOE_F32, n))
-    rc = _on_device(dev, stream, lambda st: load_library().moe_combine_backward(
-        ctypes.byref(shape), _ptr(dout), _ptr(y), _ptr(inv), _ptr(weights), _ptr(dy), _ptr(dweights), st))
-    if check and rc:
-        raise MoeError(rc, "moe_combine_backward")
-    return rc
+    types, where = _torch_types(), "moe_combine_backward"
+    T, H = shape.T, shape.H
+    n, dev, yt = T * shape.top_k, _device_of(dout, y, inv), types.get(shape.y_dtype)
+    return _launch(where, load_library().moe_combine_backward, dev, stream, check, ctypes.byref(shape),
+                   _checked(where, "dout", dout, types.get(shape.out_dtype), T * H, dev),
+                   _checked(where, "y", y, yt, shape.rows * H, dev),
+                   _checked(where, "inv", inv, types["i32"], n, dev),
+                   _checked(where, "weights", weights, types[MOE_F32], n, dev),
+                   _checked(where, "dy", dy, yt, shape.rows * H, dev),
+                   _checked(where, "dweights", dweights, types[MOE_F32], n, dev))

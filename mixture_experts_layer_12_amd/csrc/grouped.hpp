@@ -89,8 +89,9 @@ struct GroupedArgs {
   const float* x_scale;     // 8-bit: [x_rows]
   const float* w_scale;     // 8-bit: [E, N]
   const uint64_t* row_table;   // dw on large tiles: addresses of the rows of x in sorted order (workspace)
-  float* parts;             // forward and dx on large tiles: sums of items cut along the reduction (workspace)
-  int max_parts;            // ... the most parts of one item
+  float* parts;             // sums of tiles that are cut along the reduction (workspace)
+  int max_parts;            // ... the most parts of a tile (large tiles), or the parts of every tile
+  size_t part_size;         // ... values between the parts of a tile (the other kernel)
   int rows, N, K, E, x_rows, row_div;
   unsigned div_mul;         // n / row_div = mulhi(2 n, div_mul) >> div_shift for 0 <= n < 2^31
   int div_shift;
