@@ -8,16 +8,22 @@
 // The waves of a work-group share 16 R weight rows and cut K between them, so
 // that many loads are in flight for every row even when there are few tiles;
 // their partial sums meet in LDS and are added in a fixed order.  A segment is
-// taken 64 rows at a time (C = 1, 2 or 4 column tiles of 16 rows).
+// taken 32 rows at a time (C = 1 or 2 column tiles of 16 rows): with more, the
+// registers would leave room for too few waves to keep HBM busy.
 // Rows of any alignment: 16-byte loads need none here.
+#include <algorithm>
+#include <type_traits>
+
 #include "grouped.hpp"
 
 namespace moe {
 
 namespace {
 
-constexpr int GS_ROWS = 64;              // sorted rows per item
-constexpr int GS_UNROLL = 8;             // k-steps in flight per wave
+constexpr int GS_ROWS = 32;              // sorted rows per item
+// 16-byte loads that a lane has under way: more take registers from waves (eight tokens through 8 experts of
+// 14336 x 4096: 12 loads 172 us, 18 175, 24 182)
+constexpr int GS_LOADS = 12;
 
 template <int DT> struct Small;
 template <> struct Small<DT_F32> { typedef f32x4_t acc; };
@@ -36,10 +42,9 @@ __device__ __forceinline__ void mma16x16(u32x4_t w, u32x4_t x, Acc& c) {
   }
 }
 
-// n_tiles tiles of R x 16 weight rows from n0, C x 16 rows of x; wave `wv` of W takes its share of K.
+// R x 16 weight rows from n0, C x 16 rows of x; wave `wv` of W takes its share of K.
 template <int DT, int OUT, int R, int C, int W>
-__device__ __forceinline__ void stream_tiles(const GroupedArgs& a, float* smem, int e, int row0, int rows, int n0,
-                                             int n_tiles) {
+__device__ __forceinline__ void stream_tile(const GroupedArgs& a, float* smem, int e, int row0, int rows, int n0) {
   typedef typename Elem<DT>::type T;
   typedef typename Small<DT>::acc Acc;
   constexpr int E16 = 16 / int(sizeof(T));                     // values per 16 bytes
@@ -54,7 +59,6 @@ __device__ __forceinline__ void stream_tiles(const GroupedArgs& a, float* smem, 
     const int src = m < rows ? source_row(a, row0 + m) : -1;
     px[c] = (src < 0 ? w : reinterpret_cast<const T*>(a.x) + size_t(src) * a.K) + g * E16;
   }
-  for (int tile = 0; tile < n_tiles; ++tile, n0 += 16 * R) {
   const T* pw[R];                                // weight rows past N read the tile's first row
 #pragma unroll
   for (int r = 0; r < R; ++r) pw[r] = w + size_t(n0 + 16 * r + l16 < a.N ? n0 + 16 * r + l16 : n0) * a.K + g * E16;
@@ -69,31 +73,31 @@ __device__ __forceinline__ void stream_tiles(const GroupedArgs& a, float* smem, 
   constexpr int S = 4 * E16;                                   // values per k-step
   const int full = a.K / S;                                    // whole k-steps
   const int s_begin = int(long(full) * wv / W), s_end = int(long(full) * (wv + 1) / W);
+  // groups of U k-steps, whose loads are all under way before the first product; in the last group the loads
+  // past the end repeat the last step, and their products are left out
+  constexpr int U = GS_LOADS / (R + C) < 8 ? GS_LOADS / (R + C) : 8;
+  auto group = [&](int s, auto whole) {
+    u32x4_t fw[U][R], fx[U][C];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const size_t at = size_t(decltype(whole)::value ? s + u : min(s + u, s_end - 1)) * S;
+#pragma unroll
+      for (int r = 0; r < R; ++r) fw[u][r] = load16(pw[r] + at);
+#pragma unroll
+      for (int c = 0; c < C; ++c) fx[u][c] = load16(px[c] + at);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (decltype(whole)::value || s + u < s_end) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int c = 0; c < C; ++c) mma16x16<DT>(fw[u][r], fx[u][c], acc[r][c]);
+      }
+  };
   int s = s_begin;
-  for (; s + GS_UNROLL <= s_end; s += GS_UNROLL) {
-    u32x4_t fw[GS_UNROLL][R], fx[GS_UNROLL][C];
-#pragma unroll
-    for (int u = 0; u < GS_UNROLL; ++u) {
-#pragma unroll
-      for (int r = 0; r < R; ++r) fw[u][r] = load16(pw[r] + size_t(s + u) * S);
-#pragma unroll
-      for (int c = 0; c < C; ++c) fx[u][c] = load16(px[c] + size_t(s + u) * S);
-    }
-#pragma unroll
-    for (int u = 0; u < GS_UNROLL; ++u)
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int c = 0; c < C; ++c) mma16x16<DT>(fw[u][r], fx[u][c], acc[r][c]);
-  }
-  for (; s < s_end; ++s) {
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const u32x4_t fw = load16(pw[r] + size_t(s) * S);
-#pragma unroll
-      for (int c = 0; c < C; ++c) mma16x16<DT>(fw, load16(px[c] + size_t(s) * S), acc[r][c]);
-    }
-  }
+  for (; s + U <= s_end; s += U) group(s, std::true_type{});
+  if (s < s_end) group(s, std::false_type{});
   if (wv == W - 1 && full * S < a.K) {                         // the end of the rows, past the last whole step
     const int left = a.K - full * S - g * E16;
 #pragma unroll
@@ -142,55 +146,41 @@ __device__ __forceinline__ void stream_tiles(const GroupedArgs& a, float* smem, 
         if (n + i < a.N) store_out<OUT>(a.out, at + i, o[i]);
     }
   }
-  }
 }
 
-// Each work-group takes an equal, contiguous share of the (row tile, column
-// tile) items, columns inner: the look-up of the row tile, which costs as much
-// as reading tens of kilobytes, is then made once for many items.
+// A work-group per (row tile, column tile) item, columns inner, dispatched as
+// CUs fall free (resident ones with a fixed share of the items: 215 us for
+// eight tokens through 8 experts of 14336 x 4096, against 183).
 template <int DT, int OUT, int R, int W>
 __global__ void __launch_bounds__(64 * W) grouped_stream_kernel(GroupedArgs a) {
-  __shared__ __attribute__((aligned(16))) float smem[W * R * 4 * 64 * 4];
+  __shared__ __attribute__((aligned(16))) float smem[W * R * (GS_ROWS / 16) * 64 * 4];
   const int n_ct = (a.N + 16 * R - 1) / (16 * R);
-  long item, end;
-  RowTile rt;
-  {
+  for (long item = blockIdx.x;; item += gridDim.x) {
     const RowTiles tiles(a, GS_ROWS);
-    const long n_items = long(tiles.total) * n_ct;
-    item = n_items * blockIdx.x / gridDim.x;
-    end = n_items * (blockIdx.x + 1) / gridDim.x;
-    if (item >= end) return;
-    rt = tiles.at(int(item / n_ct), GS_ROWS);
-  }
-  int ct = int(item % n_ct);
-  while (true) {
-    const int n = int(min(long(n_ct - ct), end - item));          // items of this row tile
-    const int rows = min(rt.n, GS_ROWS);
-    if (rows <= 16) stream_tiles<DT, OUT, R, 1, W>(a, smem, rt.e, rt.begin, rows, ct * 16 * R, n);
-    else if (rows <= 32) stream_tiles<DT, OUT, R, 2, W>(a, smem, rt.e, rt.begin, rows, ct * 16 * R, n);
-    else stream_tiles<DT, OUT, R, 4, W>(a, smem, rt.e, rt.begin, rows, ct * 16 * R, n);
-    item += n;
-    if (item >= end) return;
-    ct = 0;
-    rt = RowTiles(a, GS_ROWS).at(int(item / n_ct), GS_ROWS);
+    if (item >= long(tiles.total) * n_ct) return;
+    const RowTile rt = tiles.at(int(item / n_ct), GS_ROWS);
+    const int rows = min(rt.n, GS_ROWS), n0 = int(item % n_ct) * 16 * R;
+    if (rows <= 16) stream_tile<DT, OUT, R, 1, W>(a, smem, rt.e, rt.begin, rows, n0);
+    else stream_tile<DT, OUT, R, 2, W>(a, smem, rt.e, rt.begin, rows, n0);
   }
 }
 
-template <int DT, int OUT, int R, int W>
-hipError_t launch_rw(const GroupedArgs& a, int per_cu, hipStream_t st) {
-  const long n_items = (long(a.rows) / GS_ROWS + (a.rows < a.E ? a.rows : a.E)) * ((a.N + 16 * R - 1) / (16 * R));
-  const long most = 256L * per_cu;
-  hipLaunchKernelGGL((grouped_stream_kernel<DT, OUT, R, W>), dim3(unsigned(n_items < most ? n_items : most)),
-                     dim3(64 * W), 0, st, a);
+// Row tiles at most.
+long stream_row_tiles(const GroupedArgs& a) { return long(a.rows) / GS_ROWS + std::min(a.E, a.rows); }
+
+template <int DT, int OUT, int R>
+hipError_t launch_r(const GroupedArgs& a, hipStream_t st) {
+  const long n_items = stream_row_tiles(a) * ((a.N + 16 * R - 1) / (16 * R));
+  hipLaunchKernelGGL((grouped_stream_kernel<DT, OUT, R, 4>), dim3(unsigned(std::min(n_items, 1L << 22))), dim3(64 * 4), 0,
+                     st, a);
   return hipGetLastError();
 }
 
 template <int DT, int OUT>
 hipError_t launch_stream(const GroupedArgs& a, hipStream_t st) {
-  // Two weight rows tiles a wave halve the reads of x, once there are work-groups enough without.
-  const long tiles16 = (long(a.rows) / GS_ROWS + (a.rows < a.E ? a.rows : a.E)) * ((a.N + 15) / 16);
-  if (tiles16 >= 2048) return launch_rw<DT, OUT, 2, 4>(a, 3, st);
-  return launch_rw<DT, OUT, 1, 8>(a, 2, st);
+  // Two tiles of weight rows a wave halve the reads of x, once there are work-groups enough without.
+  if (stream_row_tiles(a) * ((a.N + 15) / 16) >= 2048) return launch_r<DT, OUT, 2>(a, st);
+  return launch_r<DT, OUT, 1>(a, st);
 }
 
 }  // namespace
