@@ -130,6 +130,41 @@ def test_sizes(m, N, K, x):
     Case([3, 0, 140], N, K, x, x, seed=N * 31 + K).check(m)
 
 
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("counts", [[1, 0, 63, 64], [65, 128, 129], [255, 256, 257, 0, 5], [600]])
+@pytest.mark.parametrize("N, K", [(1032, 1096), (1288, 1024), (1100, 2056)])
+def test_long_reductions(m, N, K, counts, out):
+    """Both products of at least 16 stages: large tiles of every height, whole and cut along the reduction, whose
+    ends lie inside a stage and inside a tile; rows behind and between the segments stay."""
+    Case(counts, N, K, "bf16", out, pad=3, extra_rows=9, seed=N + len(counts)).check(m)
+    ids = lambda rng, rows: rng.integers(-3, 2 * 70 + 9, rows)
+    Case(counts, N, K, "bf16", out, pad=2, ids=ids, row_div=2, x_rows=70, seed=N).check(m)
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("lookup_rows", [False, True])
+@pytest.mark.parametrize("N, K", [(264, 520), (512, 256), (40, 1288)])
+def test_weight_gradients_of_many_tiles(m, N, K, lookup_rows, out):
+    """Enough tiles of dw for the resident work-groups: segments of no row, of a part of a stage, of whole stages."""
+    counts = [0, 1, 63, 64, 65, 127, 128, 129, 190, 200, 3] * 6
+    kw = dict(ids=lambda rng, rows: rng.integers(-9, 3 * 500 + 40, rows), row_div=3, x_rows=500) if lookup_rows else {}
+    c = Case(counts, N, K, "bf16", out, pad=4, extra_rows=5, seed=N, **kw)
+    xs, dy = G.lookup(H.to_f64(c.x), c.ids, c.row_div, c.rows), H.to_f64(c.dy)
+    w = np.zeros((c.E, N, K))
+    gw = H.to_f64(c.backward(m, dx=False)[1])
+    rw, aw = (G.grouped_matmul_backward(a, b, c.segs, w)[1] for a, b in ((dy, xs), (abs(dy), abs(xs))))
+    close(gw, rw, aw, 200, out)
+    assert (gw[0] == 0).all()
+
+
+@pytest.mark.parametrize("x", ["bf16", "f32"])
+def test_few_tiles_are_cut(m, x):
+    """Small outputs of long reductions, aligned and not: the parts add up, dw of short segments among them."""
+    for N, K, counts in ((3, 5001, [2, 0, 40]), (5001, 3, [70, 1]), (16, 24, [3000, 0, 700, 5]), (17, 23, [2500, 9]),
+                         (2000, 40, [33, 35]), (64, 4104, [200, 3])):
+        Case(counts, N, K, x, x, pad=2, extra_rows=3, seed=K).check(m)
+
+
 @pytest.mark.parametrize("x", ["bf16", "f32"])
 def test_padded_order_and_lookup(m, x):
     """moe_route's padded order: sentinel ids in the padding, rows looked up twice, never or outside x."""
@@ -280,6 +315,15 @@ def test_i8_sizes(m, N, K, out):
     i8_case(m, [2, 1, 0], N, K, out, seed=N + K)
 
 
+@pytest.mark.parametrize("counts", [[1, 0, 63, 64], [65, 128, 129], [255, 256, 257, 0, 5]])
+@pytest.mark.parametrize("N, K", [(264, 2064), (1000, 2048), (37, 4000), (37, 4001)])
+def test_i8_long_reductions(m, N, K, counts):
+    """Large tiles whole and cut (and the other kernel's cuts): sums of parts stay exact."""
+    ids = lambda rng, rows: rng.integers(-3, 2 * 70 + 9, rows)
+    i8_case(m, counts, N, K, pad=3, extra_rows=9)
+    i8_case(m, counts, N, K, out="f32", pad=2, ids=ids, row_div=2, x_rows=70)
+
+
 def test_i8_lookup(m):
     ids = lambda rng, rows: rng.integers(-4, 3 * 50 + 30, rows)
     i8_case(m, [5, 0, 130, 128], 72, 96, pad=128, ids=ids, row_div=3, x_rows=50)
@@ -339,17 +383,18 @@ def test_on_another_stream(m):
     assert torch.equal(y, want)
 
 
-@pytest.mark.parametrize("N, K", [(264, 1024), (37, 61)])
-def test_captured_into_a_graph(m, N, K):
+@pytest.mark.parametrize("N, K, many", [(264, 1024, 0), (37, 61, 0), (1288, 1032, 0), (3, 5001, 0), (264, 520, 60)])
+def test_captured_into_a_graph(m, N, K, many):
     """Captured once and replayed on new inputs and new tables, with eager work between the replays."""
-    c = Case([40, 0, 5, 129], N, K, extra_rows=60)
+    ids = lambda rng, rows: rng.permutation(rows)
+    c = Case([40, 0, 5, 129] + [0] * many, N, K, extra_rows=60, ids=ids, x_rows=40 + 5 + 129 + 60)
     s = c.shape(m)
     y, gx, gw = c.forward(m), *c.backward(m)
     ws = c.ws(m, s)
 
     def step():
-        m.moe_grouped_matmul(s, c.x, None, c.offsets, c.counts, c.w, y, ws)
-        m.moe_grouped_matmul_backward(s, c.dy, c.x, None, c.offsets, c.counts, c.w, gx, gw, ws)
+        m.moe_grouped_matmul(s, c.x, c.ids_t, c.offsets, c.counts, c.w, y, ws)
+        m.moe_grouped_matmul_backward(s, c.dy, c.x, c.ids_t, c.offsets, c.counts, c.w, gx, gw, ws)
 
     step()
     torch.cuda.synchronize()
@@ -358,7 +403,7 @@ def test_captured_into_a_graph(m, N, K):
         step()
     rng = np.random.default_rng(3)
     for i in range(4):
-        cnt = rng.integers(0, 58, 4)
+        cnt = rng.integers(0, 58, 4) if not many else rng.integers(0, 4, 4 + many)
         off = np.concatenate([[0], np.cumsum(cnt)])
         c.offsets.copy_(dev(off.astype(np.int32)))
         c.counts.copy_(dev(cnt.astype(np.int32)))
