@@ -4,7 +4,12 @@ Argument marshalling only: every step of the layer runs in the HIP kernels of
 ``lib/libmoe.so``.  Functions carry the C names (``moe_workspace_size``,
 ``moe_dispatch_dims``, ``moe_route``, ``moe_forward``, ``moe_strerror``) and
 accept torch tensors (their ``data_ptr()`` is passed) or raw integer device
-addresses.  PyTorch only provides device memory and the current stream.
+addresses.  The separate operators (``moe_grouped_matmul`` and its gradients,
+``moe_quantize_rows``, ``moe_grouped_matmul_i8``, ``moe_combine`` and its
+gradients) also check that the tensors they are given are dense, on one GPU
+and of the type and size that the shape says, and run on the current stream of
+that GPU unless they are given one.  PyTorch only provides device memory and
+the current stream.
 
 There is no fallback: if the library is missing the calls raise.
 """
@@ -520,6 +525,8 @@ def _grouped(where, function, shape, x_name, x, x_scale, dy, row_ids, offsets, c
     else:
         args = (px, ids, off, cnt, pw)
     nb = _nbytes(workspace) if ws_bytes is None else ws_bytes
+    if workspace is not None and type(workspace) is not int and dev is not None and workspace.get_device() != dev:
+        raise ValueError(f"{where}: workspace is not on the operands' GPU")
     return _launch(where, function, dev, stream, check, ctypes.byref(shape), *args, *po, _ptr(workspace), nb)
 
 
