@@ -440,7 +440,10 @@ typedef struct {
 } moe_grouped_shape_t;
 
 /* Bytes of workspace that the calls with shape *s need (the most any of them
- * does; host call, no GPU access). */
+ * does; host call, no GPU access).  It holds the partial sums of reductions
+ * that are cut to fill the chip (at most 64 MiB) and, for dw, 8 bytes for each
+ * sorted row and a row of x; many shapes need none.  Calls that may run at the
+ * same time (other streams, captured graphs) need workspaces of their own. */
 int moe_grouped_workspace_size(const moe_grouped_shape_t* s, size_t* bytes /* host */);
 
 /* y[r, n] = sum_k x[row(r), k] * w[e, n, k] for the rows r of each expert e.
@@ -455,7 +458,8 @@ int moe_grouped_matmul(const moe_grouped_shape_t* s, const void* x, const int32_
  *   dw[e, n, k] = sum over e's rows r of dy[r, n] * x[row(r), k]     dw [E, N, K], out_dtype
  * dx or dw may be NULL (not both, while there are rows): that gradient is not formed, and w (needed
  * for dx only) or x and row_ids (needed for dw only) may be NULL with it.
- * dw is written whole; experts without rows get zeros.  The gradient of a
+ * dw is written whole; experts without rows get zeros, and a row that row_ids
+ * stands for zeros adds nothing, whatever its dy holds.  The gradient of a
  * gathered x is moe_combine of dx with weights NULL. */
 int moe_grouped_matmul_backward(const moe_grouped_shape_t* s, const void* dy, const void* x,
                                 const int32_t* row_ids, const int32_t* offsets, const int32_t* counts,
@@ -476,7 +480,7 @@ int moe_quantize_rows(int32_t rows, int32_t cols, int32_t x_dtype, const void* x
  *   xq int8 [x_rows, K], x_scale f32 [x_rows] (moe_quantize_rows);
  *   wq int8 [E, N, K], w_scale f32 [E, N]; y [rows, N]
  * The sum is exact; the scales are applied in fp32, x_scale first.  A row
- * that row_ids stands for zeros has the product 0. */
+ * that row_ids stands for zeros has the product 0, whatever w_scale holds. */
 int moe_grouped_matmul_i8(const moe_grouped_shape_t* s, const int8_t* xq, const float* x_scale,
                           const int32_t* row_ids, const int32_t* offsets, const int32_t* counts,
                           const int8_t* wq, const float* w_scale, void* y, void* workspace, size_t ws_bytes,

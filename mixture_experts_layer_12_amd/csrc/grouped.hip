@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(ATHREADS) grouped_any_kernel(GroupedArgs a) {
         const int m = m0 + r;
         const int src = m >= m_end ? -1 : (WHICH == GM_FORWARD ? source_row(a, m) : m);
         pa[i] = src < 0 ? nullptr : (WHICH == GM_FORWARD ? x + size_t(src) * a.K : dy + size_t(src) * a.N);
-        if (WHICH == GM_FORWARD && tid % CPQ == 0) row_scale[r] = src < 0 ? 0.f : (DT == DT_I8 ? a.x_scale[src] : 1.f);
+        if (WHICH == GM_FORWARD && tid % CPQ == 0) row_scale[r] = scale_of<DT>(a, src);
       }
       if constexpr (BQ) pb[i] = n0 + r < n_cols ? w + size_t(n0 + r) * a.K : nullptr;
     }
@@ -147,7 +147,10 @@ __global__ void __launch_bounds__(ATHREADS) grouped_any_kernel(GroupedArgs a) {
     };
     auto load = [&](int q0) {
       if constexpr (AQ) load_q(pa, q0, ra);
-      else load_m([&](int q) { return dy + size_t(row0 + q) * a.N; }, m0, m_end, q0, ra);
+      else
+        load_m([&](int q) {                       // rows that stand for zeros add nothing, whatever dy holds there
+          return source_row(a, row0 + q) < 0 ? (const T*)nullptr : dy + size_t(row0 + q) * a.N;
+        }, m0, m_end, q0, ra);
       if constexpr (BQ) load_q(pb, q0, rb);
       else if constexpr (WHICH == GM_GRAD_X) load_m([&](int q) { return w + size_t(q) * a.K; }, n0, n_cols, q0, rb);
       else
@@ -215,8 +218,8 @@ __global__ void __launch_bounds__(ATHREADS) grouped_any_kernel(GroupedArgs a) {
             continue;
           }
           float v;
-          if constexpr (DT == DT_I8) v = float(acc[i][j][q]) * row_scale[r] * ws;
-          else v = WHICH == GM_FORWARD && row_scale[r] == 0.f ? 0.f : acc[i][j][q];   // rows that stand for zeros
+          if constexpr (DT == DT_I8) v = is_no_row(row_scale[r]) ? 0.f : float(acc[i][j][q]) * row_scale[r] * ws;
+          else v = WHICH == GM_FORWARD && is_no_row(row_scale[r]) ? 0.f : acc[i][j][q];   // rows that stand for zeros
           store_out<OUT>(a.out, at, v);
         }
     }

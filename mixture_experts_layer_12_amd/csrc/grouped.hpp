@@ -121,6 +121,17 @@ __device__ __forceinline__ int source_row(const GroupedArgs& a, int r) {
   return source_of(a, a.row_ids[r]);
 }
 
+// Scale of row src of x: x_scale (8-bit) or 1.  A row of zeros (src < 0) has
+// -0 (no scale is passed on as -0): its product is 0 whatever w_scale holds.
+template <int DT>
+__device__ __forceinline__ float scale_of(const GroupedArgs& a, int src) {
+  if (src < 0) return -0.f;
+  if constexpr (DT != DT_I8) return 1.f;
+  const uint32_t s = __float_as_uint(a.x_scale[src]);
+  return __uint_as_float(s == 0x80000000u ? 0u : s);
+}
+__device__ __forceinline__ bool is_no_row(float scale) { return __float_as_uint(scale) == 0x80000000u; }
+
 // The list that holds ceil(n / tile) row tiles for each expert's segment, in
 // order.  Every wave looks it up for itself: four experts a lane, with a
 // prefix sum over the lanes.

@@ -474,3 +474,50 @@ def test_rows_past_32_bit_offsets(m):
         ref = g @ b
         assert ((dx[r].double().cpu() - ref).abs()
                 <= HALF["bf16"] * ref.abs() + 8 * N ** 0.5 * 2.0 ** -23 * (g.abs() @ b.abs())).all(), r
+
+
+@pytest.mark.parametrize("x, N, K", [("bf16", 67, 61), ("f32", 67, 61), ("bf16", 96, 64), ("bf16", 2048, 2048)])
+def test_rows_of_zeros_add_nothing_to_the_weight_gradient(m, x, N, K):
+    """Rows whose row_ids name no row of x: NaN and infinities in their dy do not reach dw, on small tiles and on large
+    ones, in the first, whole and last stages of a segment."""
+    def ids(rng, rows):
+        v = rng.integers(0, 40, rows)
+        v[::7] = -1
+        v[5::11] = 40
+        v[:3] = -1
+        return v
+    c = Case([70, 330], N, K, x, "f32", ids=ids, row_div=1, x_rows=40, seed=N)
+    none = (c.ids < 0) | (c.ids >= 40)
+    dy = H.to_f64(c.dy)
+    dy[none] = 0
+    xs = G.lookup(H.to_f64(c.x), c.ids, 1, c.rows)
+    rw = G.grouped_matmul_backward(dy, xs, c.segs, H.to_f64(c.w))[1]
+    aw = G.grouped_matmul_backward(abs(dy), abs(xs), c.segs, abs(H.to_f64(c.w)))[1]
+    at = np.flatnonzero(none)
+    c.dy[dev(at[::2])] = float("nan")
+    c.dy[dev(at[1::2])] = float("inf")
+    close(H.to_f64(c.backward(m, dx=False)[1]), rw, aw, 330, "f32")
+
+
+@pytest.mark.parametrize("counts, N, K", [([5, 3], 64, 64), ([130, 128], 72, 89), ([130, 128], 37, 4001),
+                                          ([130, 128], 264, 2064), ([130, 128], 22016, 64)])
+def test_i8_rows_of_zeros_stay_zero(m, counts, N, K):
+    """A row that row_ids stands for zeros has the product 0 for scales of infinity and NaN too; a row of x with the
+    scale 0 or -0 has the formula's NaN."""
+    rows = sum(counts)
+    c = Case(counts, 1, 1, "bf16", "f32")
+    ids = np.arange(rows, dtype=np.int32) % 8
+    ids[::3] = -1
+    xs = np.full(8, 0.5, dtype=np.float32)
+    xs[4], xs[5] = 0.0, -0.0
+    ws = np.full((2, N), np.inf, dtype=np.float32)
+    ws[:, ::2] = np.nan
+    s = m.make_grouped_shape(rows, N, K, 2, 8, 1, "i8", "f32")
+    y = torch.full((rows, N), SENTINEL, dtype=torch.float32, device="cuda")
+    one = torch.ones
+    m.moe_grouped_matmul_i8(s, one(8, K, dtype=torch.int8, device="cuda"), dev(xs), dev(ids), c.offsets, c.counts,
+                            one(2, N, K, dtype=torch.int8, device="cuda"), dev(ws), y, c.ws(m, s))
+    y = y.cpu().numpy()
+    assert (y[ids < 0] == 0).all()
+    assert np.isnan(y[(ids == 4) | (ids == 5)]).all()
+    assert np.isnan(y[ids == 0][:, ::2]).all() and np.isposinf(y[ids == 0][:, 1::2]).all()
