@@ -611,7 +611,9 @@ RowsPlan rows_plan(const GroupedArgs& a, int which, int in_dt) {
   const long n_cols = which == GM_FORWARD ? a.N : a.K, n_q = which == GM_FORWARD ? a.K : a.N;
   const long stages = (n_q * (in_dt == DT_I8 ? 1 : 2) + GT_STAGE - 1) / GT_STAGE;
   RowsPlan p{(long(a.rows) / 256 + std::min(a.E, a.rows)) * ((n_cols + GT_N - 1) / GT_N), 1};
-  // With many rounds the CUs that idle in the last one matter little, and the second launch is saved.
+  // With many rounds the CUs that idle in the last one matter little, and the second launch and the parts' sums are
+  // saved (9 rounds, 4096 tokens through 8 experts of 14336 x 4096: 870 us, 886 cut; in 8 bits 505 and 511; 3 rounds
+  // and less: that prompt's gradients 2000 us, 2215 uncut; 64 experts of 1408 x 2048, 1024 tokens, 253 and 270).
   if (p.items <= GT_MAXSPLIT * 8 * GT_P) p.max_parts = int(std::max<long>(1, std::min<long>(stages / GT_MIN_PART, GT_P)));
   return p;
 }
