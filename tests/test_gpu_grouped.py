@@ -521,3 +521,11 @@ def test_i8_rows_of_zeros_stay_zero(m, counts, N, K):
     assert (y[ids < 0] == 0).all()
     assert np.isnan(y[(ids == 4) | (ids == 5)]).all()
     assert np.isnan(y[ids == 0][:, ::2]).all() and np.isposinf(y[ids == 0][:, 1::2]).all()
+
+
+def test_a_workspace_off_the_gpu_is_refused(m):
+    c = Case([5, 3], 64, 64)
+    s = c.shape(m)
+    y = torch.empty(c.rows, c.N, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError, match="workspace"):
+        m.moe_grouped_matmul(s, c.x, None, c.offsets, c.counts, c.w, y, torch.empty(1 << 20, dtype=torch.uint8))
